@@ -64,7 +64,9 @@ typedef enum {
   S4R_ERR_WORKSPACE = 6     /* workspace pointer null or smaller than required */
 } s4r_status;
 
-typedef enum { S4R_F32 = 0, S4R_BF16 = 1 } s4r_dtype;
+/* S4R_FP4 is a storage type of the paged latent cache only (see
+ * s4r_latent_write); every other tensor is S4R_F32 or S4R_BF16. */
+typedef enum { S4R_F32 = 0, S4R_BF16 = 1, S4R_FP4 = 2 } s4r_dtype;
 
 /* How the query window forms scoring rows (Eqs. 8-10).
  * CONCAT (default): W*G rows; row (w, j) concatenates query head g*G + j of
@@ -91,6 +93,10 @@ typedef enum { S4R_POOL_MAX = 0, S4R_POOL_AVG = 1 } s4r_pool_mode;
 #define S4R_MAX_SINKS 16        /* n_sink */
 #define S4R_MAX_SELECTED 8192   /* top_k + local_window */
 #define S4R_MAX_BASIS_SAMPLE 1048576  /* n_sample T' of s4r_build_basis */
+#define S4R_MAX_REQUESTS 8192   /* batch of s4r_page_plan and s4r_latent_attend */
+#define S4R_MAX_LATENT_WIDTH 576  /* values a token of a latent cache (rank + rotary part) */
+#define S4R_MAX_LATENT_RANK 512 /* leading values of a latent row that form the attended value */
+#define S4R_MAX_PAGE_SIZE 1024  /* tokens a page: a power of two from 16 */
 
 /* ------------------------------------------------------------------ encode */
 
@@ -285,6 +291,207 @@ s4r_status s4r_decode_step_noalloc(const s4r_decode_args *args, void *stream);
 s4r_status s4r_reconstruct(const void *coeffs, int64_t n_rows_total, const void *basis,
                            int32_t d_model, int32_t rank, const int32_t *rows, int64_t n,
                            float *out, s4r_dtype dtype, void *stream);
+
+/* ------------------------------------------------- paged latent attention */
+
+/* Library extension: attention over EVERY token of a cache that keeps one
+ * latent vector a token, shared by all heads (next to s4r_decode_step, which
+ * attends over a chosen few of its coefficient rows).  With basis_k, basis_v
+ * [n_heads*head_dim][rank] (the layout of the decode bases, one group of rows
+ * a head) and latents c [rank], optionally followed by a rotary key part
+ * k_r [rope] that needs no basis:
+ *   key_h = (basis_k[h] . c, k_r),  value_h = basis_v[h] . c.
+ * Expanded form (prompts): keys and values are expanded with
+ * s4r_latent_project and attended with s4r_prefill_attend.  Absorbed form
+ * (decode): since q_h . (basis_k[h] c) = (q_h . basis_k[h]) . c, the queries
+ * are projected into latent space (s4r_latent_project), s4r_latent_attend
+ * attends over the cached latents themselves, and s4r_latent_project expands
+ * the attended latents with basis_v.
+ *
+ * The cache is paged: pages of page_size token rows; request b's position p
+ * is row p % page_size of page block_table[b][p / page_size], and
+ * slot = page * page_size + row names a row of the whole cache.
+ * s4r_page_plan hands out pages and computes slots, s4r_latent_write stores
+ * rows.
+ *
+ * A page of a S4R_BF16 cache is [page_size][width].  A page of a S4R_FP4
+ * cache is page_size * width * 9 / 16 bytes: the codes [page_size][width/2]
+ * (two 4-bit values a byte, the even column in the low bits), then the scales
+ * [page_size][width/16] (one e4m3 scale for 16 columns).  Column j of a row
+ * stands for e2m1(code_j) * scale_{j/16} * cache_scale, e2m1 having the
+ * magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6 and a sign bit. */
+
+/* Block tables and slot maps of a step, from request lengths, on the device.
+ * Request b holds old = lengths[b] tokens and gets new = new_tokens[b] more;
+ * have = ceil(old / page_size) pages are listed in its row of block_table.
+ * With need_b = ceil((old + new) / page_size) - have and D_b the sum of
+ * need_0 .. need_b, request b is SERVED if old, new >= 0, old + new <=
+ * max_pages * page_size and (need_b == 0 or D_b <= free); a request that fails
+ * the first two counts has need_b = 0.  Pages leave the free list from its
+ * end, in request order: entry have + i of a served request becomes
+ * free_pages[free - 1 - (D_b - need_b + i)].  Entries before `have` and behind
+ * the new ones are left as they are.
+ *   lengths_out[b]    = old + new of a served request, else old
+ *   free_count_out[0] = free - (pages handed out)
+ *   cu_tokens[b]      = new_0 + .. + new_{b-1} (negative counts as 0), b <= batch
+ * and for token t of the flat batch (the j-th new token of request b, t =
+ * cu_tokens[b] + j, whether b is served or not):
+ *   slots[t]     = block_table[b][p / page_size] * page_size + p % page_size,
+ *                  p = old + j; -1 if b is not served
+ *   positions[t] = p, requests[t] = b
+ * Entries of the three from cu_tokens[batch] to max_tokens - 1 become -1, so
+ * a captured call with a fixed max_tokens serves any step.
+ * lengths_out may be `lengths` and free_count_out may be `free_count` (the
+ * state of a serving loop, updated in place); no other buffers may overlap.
+ * Device status (S4R_ERR_DEVICE, in status_workspace if given): a request is
+ * not served, the new tokens do not fit max_tokens (the rest is not
+ * written), or free_count lies outside [0, free_capacity] (it is clamped). */
+typedef struct {
+  int32_t batch;                /* <= S4R_MAX_REQUESTS */
+  int32_t page_size, max_pages; /* block_table row length */
+  int32_t free_capacity;        /* entries of free_pages */
+  int64_t max_tokens;           /* entries of slots, positions, requests */
+  const int32_t *lengths;       /* [batch] tokens held before the step */
+  const int32_t *new_tokens;    /* [batch] */
+  int32_t *block_table;         /* [batch][max_pages] */
+  const int32_t *free_pages;    /* [free_capacity] ids of free pages, the next one last */
+  const int32_t *free_count;    /* [1] how many of them are free */
+  int32_t *lengths_out;         /* [batch] */
+  int32_t *free_count_out;      /* [1] */
+  int32_t *cu_tokens;           /* [batch + 1] */
+  int64_t *slots;               /* [max_tokens] */
+  int32_t *positions;           /* [max_tokens], or NULL */
+  int32_t *requests;            /* [max_tokens], or NULL */
+  void *status_workspace;       /* a workspace (its status word), or NULL */
+} s4r_page_plan_args;
+
+s4r_status s4r_page_plan(const s4r_page_plan_args *args, void *stream);
+
+/* Store latent rows in a paged cache: row slots[t] = latents[t].  A slot of
+ * -1 (any negative one) is skipped; a slot of n_pages * page_size or above is
+ * skipped and sets the device status (S4R_ERR_DEVICE).  Slots must differ
+ * from one another: what a row named twice holds afterwards is not defined.
+ * S4R_BF16: the values as they are.  S4R_FP4, for each 16 columns, with
+ * fp32 arithmetic and x = latent / cache_scale:
+ *   scale = e4m3(min(max|x| / 6, 448)), code = e2m1(x / scale), both to
+ *   nearest, ties to even, |x / scale| > 6 to 6; a scale of 0 has codes 0.
+ * Infinities therefore become +-6 * scale, NaN becomes 6 * scale.  `stored`
+ * (optional, S4R_FP4) gets the values that the cache now stands for, rounded
+ * to bf16 (exact when cache_scale is a power of two), skipped rows included. */
+typedef struct {
+  int64_t n_tokens;
+  int32_t width;             /* multiple of 8 (S4R_BF16) or 32 (S4R_FP4) */
+  int32_t page_size;
+  int64_t n_pages;
+  s4r_dtype cache_dtype;     /* S4R_BF16 or S4R_FP4 */
+  float cache_scale;         /* S4R_FP4: > 0; ignored for S4R_BF16 */
+  const void *latents;       /* [n_tokens][width] bf16 */
+  int64_t latents_ld;        /* row stride in elements, a multiple of 8 */
+  const int64_t *slots;      /* [n_tokens] */
+  void *cache;               /* [n_pages] pages */
+  void *stored;              /* [n_tokens][width] bf16 contiguous, or NULL */
+  void *status_workspace;    /* a workspace (its status word), or NULL */
+} s4r_latent_write_args;
+
+s4r_status s4r_latent_write(const s4r_latent_write_args *args, void *stream);
+
+/* Attention over the cached latents (absorbed form).  Request b holds
+ * lengths[b] rows; its n_query query tokens are the last of them, so query
+ * token t sees rows 0 .. lengths[b] - n_query + t.  For every head h
+ *   z_i = scale * q[b][t][h] . row_i,  p = softmax(z),
+ *   out[b][t][h] = sum_i p_i row_i[0 .. rank-1],  lse[b][t][h] = log sum_i e^{z_i}.
+ * A query token that sees no row gets out = 0, lse = -infinity.  What lies in
+ * rows that a query does not see (NaN and infinities included) has no
+ * influence.  fp32 statistics and accumulation; probabilities are rounded to
+ * 16 bits (bf16 next to bf16 rows, fp16 next to 4-bit ones) for the value
+ * product only.
+ * Device status (S4R_ERR_DEVICE): a length outside [0, max_pages *
+ * page_size] (clamped), a page id outside [0, n_pages) among a request's
+ * pages (its rows read as zeros); S4R_ERR_TIMEOUT as elsewhere.  The outputs
+ * of such a request are not defined.
+ * Workspace: s4r_latent_attend_workspace_bytes(args) bytes, prepared once
+ * with s4r_workspace_init; calls that may overlap in time need their own. */
+typedef struct {
+  int32_t batch;             /* <= S4R_MAX_REQUESTS */
+  int32_t n_query;           /* query tokens a request (1: plain decode) */
+  int32_t n_heads;
+  int32_t width;             /* values a cache row: rank + rotary part; multiple of 8 (S4R_FP4: 32) */
+  int32_t rank;              /* leading values that are attended; multiple of 8, <= width */
+  int32_t page_size, max_pages;
+  s4r_dtype cache_dtype;     /* S4R_BF16 or S4R_FP4 */
+  int64_t n_pages;
+  float scale;               /* of the logits */
+  float cache_scale;         /* S4R_FP4: > 0; ignored for S4R_BF16 */
+  const void *q;             /* [batch][n_query][n_heads][width] bf16 */
+  const void *cache;         /* [n_pages] pages */
+  const int32_t *block_table;/* [batch][max_pages] */
+  const int32_t *lengths;    /* [batch] */
+  void *out;                 /* [batch][n_query][n_heads][rank] bf16 */
+  float *lse;                /* [batch][n_query][n_heads], or NULL */
+  void *workspace;
+  size_t workspace_bytes;
+} s4r_latent_attend_args;
+
+/* Workspace bytes for these arguments on the current device (only the shape
+ * fields are read; 0 if they are invalid). */
+size_t s4r_latent_attend_workspace_bytes(const s4r_latent_attend_args *args);
+s4r_status s4r_latent_attend(const s4r_latent_attend_args *args, void *stream);
+
+/* Per-head products between head space and latent space, bf16 with fp32
+ * accumulation, rounded once (nearest even).  With B_h = rows h*head_dim ..
+ * (h+1)*head_dim-1 of basis:
+ *   to_latent != 0: out[t][h][j] = sum_d x[t][h][d] B_h[d][j]   (absorb queries)
+ *   to_latent == 0: out[t][h][d] = sum_j x[t][h][j] B_h[d][j]   (expand latents)
+ * x_hs == 0 lets all heads share one x row a token (expanding keys or values
+ * from a token's latent).  Strides are in elements, multiples of 8; out rows
+ * must not overlap one another or the inputs. */
+typedef struct {
+  int64_t n_tokens;
+  int32_t n_heads, head_dim, rank;  /* multiples of 8; head_dim <= S4R_MAX_HEAD_DIM, rank <= S4R_MAX_LATENT_RANK */
+  int32_t to_latent;
+  const void *x;
+  int64_t x_ts, x_hs;               /* token and head strides of x */
+  const void *basis;                /* [n_heads*head_dim][rank] */
+  void *out;
+  int64_t out_ts, out_hs;           /* token and head strides of out */
+} s4r_latent_project_args;
+
+s4r_status s4r_latent_project(const s4r_latent_project_args *args, void *stream);
+
+/* Attention of ragged prompts over expanded keys and values (bf16).  Sequence
+ * b has query rows cu_q[b] .. cu_q[b+1]-1 and key rows cu_k[b] .. cu_k[b+1]-1;
+ * with nq and nk of them, query i sees keys 0 .. nk - nq + i if causal (the
+ * queries are the last tokens; a query with nk - nq + i < 0 sees none), else
+ * all.  Query head h uses kv head h / (n_heads_q / n_heads_kv):
+ *   z = scale * (q[:head_dim] . k + q[head_dim:] . k_rope),
+ *   out = softmax(z) . v, lse = log sum e^z
+ * k_rope is one row a key token for all heads (rope_dim == 0: none).  A query
+ * that sees no key gets out = 0, lse = -infinity.  fp32 statistics and
+ * accumulation, probabilities rounded to bf16 for the value product only.
+ * Rows of out and lse outside every sequence are left as they are.
+ * max_q must be at least the longest query count; it only sizes the launch.
+ * Device status (the library-wide word, s4r_read_device_status(NULL, .)):
+ * offsets that decrease or leave [0, total] (the sequence is skipped), a
+ * sequence longer than max_q (its rows from max_q on are not computed). */
+typedef struct {
+  int32_t batch;                         /* <= 65535 */
+  int32_t n_heads_q, n_heads_kv;
+  int32_t head_dim, rope_dim, value_dim; /* multiples of 8; head_dim, value_dim <= 128, rope_dim <= 64 */
+  int32_t causal;
+  int32_t max_q;
+  int64_t total_q, total_k;              /* rows of q and out; of k, v and k_rope */
+  float scale;
+  const void *q;                         /* [total_q][n_heads_q][head_dim + rope_dim] */
+  const void *k;                         /* [total_k][n_heads_kv][head_dim] */
+  const void *v;                         /* [total_k][n_heads_kv][value_dim] */
+  const void *k_rope;                    /* [total_k][rope_dim], or NULL */
+  int64_t k_ts, v_ts, k_rope_ts;         /* token strides in elements, multiples of 8 */
+  const int32_t *cu_q, *cu_k;            /* [batch + 1] device */
+  void *out;                             /* [total_q][n_heads_q][value_dim] bf16 */
+  float *lse;                            /* [total_q][n_heads_q], or NULL */
+} s4r_prefill_attend_args;
+
+s4r_status s4r_prefill_attend(const s4r_prefill_attend_args *args, void *stream);
 
 /* ------------------------------------------------------------------ status */
 

@@ -1,0 +1,192 @@
+// api_latent.cuh -- entry points of the paged latent cache and of prefill
+// attention: argument checks and launches (included by s4r_api.cu, whose
+// helpers it uses).
+#pragma once
+
+namespace {
+
+inline bool pow2(int64_t x) { return x > 0 && (x & (x - 1)) == 0; }
+inline int log2_of(int32_t x) {
+  int s = 0;
+  while ((1 << s) < x) ++s;
+  return s;
+}
+// A grid of `want` CTAs, within what a launch takes.
+inline unsigned grid_of(int64_t want, int64_t most) { return (unsigned)smax<int64_t>(1, smin<int64_t>(want, most)); }
+
+s4r_status page_size_ok(int32_t page_size) {
+  if (page_size <= 0) return S4R_ERR_INVALID_ARG;
+  return pow2(page_size) && page_size >= 16 && page_size <= S4R_MAX_PAGE_SIZE ? S4R_OK : S4R_ERR_UNSUPPORTED;
+}
+
+// Shape of a latent cache: type, width, page size, page count.
+s4r_status cache_shape_ok(s4r_dtype dt, int32_t width, int32_t page_size, int64_t n_pages, float cache_scale) {
+  if (dt != S4R_F32 && dt != S4R_BF16 && dt != S4R_FP4) return S4R_ERR_INVALID_ARG;
+  if (width <= 0 || n_pages < 0) return S4R_ERR_INVALID_ARG;
+  const s4r_status rc = page_size_ok(page_size);
+  if (rc != S4R_OK) return rc;
+  if (dt == S4R_F32 || width > S4R_MAX_LATENT_WIDTH || width % (dt == S4R_FP4 ? 32 : 8) || n_pages > INT32_MAX)
+    return S4R_ERR_UNSUPPORTED;
+  if (dt == S4R_FP4 && !(cache_scale > 0.0f && cache_scale <= 3.4e38f)) return S4R_ERR_INVALID_ARG;
+  return S4R_OK;
+}
+
+s4r_status latent_attend_shape(const s4r_latent_attend_args *a) {
+  if (!a) return S4R_ERR_INVALID_ARG;
+  const s4r_status rc = cache_shape_ok(a->cache_dtype, a->width, a->page_size, a->n_pages, a->cache_scale);
+  if (rc != S4R_OK) return rc;
+  if (a->batch < 0 || a->n_query <= 0 || a->n_heads <= 0 || a->rank <= 0 || a->rank > a->width || a->max_pages <= 0 ||
+      !std::isfinite(a->scale))
+    return S4R_ERR_INVALID_ARG;
+  if (a->rank % 8 || a->rank > S4R_MAX_LATENT_RANK || a->batch > S4R_MAX_REQUESTS ||
+      (int64_t)a->n_query * a->n_heads > INT32_MAX / S4R_MAX_LATENT_WIDTH ||
+      (int64_t)a->max_pages * a->page_size > INT32_MAX)
+    return S4R_ERR_UNSUPPORTED;
+  return S4R_OK;
+}
+
+size_t latent_attend_bytes(const s4r_latent_attend_args *) { return kAlign; }
+
+}  // namespace
+
+extern "C" {
+
+s4r_status s4r_page_plan(const s4r_page_plan_args *a, void *stream) {
+  if (!a) return S4R_ERR_INVALID_ARG;
+  if (a->batch < 0 || a->max_pages <= 0 || a->free_capacity < 0 || a->max_tokens < 0) return S4R_ERR_INVALID_ARG;
+  const s4r_status rc = page_size_ok(a->page_size);
+  if (rc != S4R_OK) return rc;
+  if (a->batch > S4R_MAX_REQUESTS || a->max_tokens > INT32_MAX || (int64_t)a->max_pages * a->page_size > INT32_MAX)
+    return S4R_ERR_UNSUPPORTED;
+  const void *must[] = {a->free_count, a->free_count_out, a->cu_tokens};
+  for (const void *p : must)
+    if (!p || !aligned16(p)) return S4R_ERR_INVALID_ARG;
+  const void *per_request[] = {a->lengths, a->new_tokens, a->block_table, a->lengths_out};
+  for (const void *p : per_request)
+    if ((a->batch > 0 && !p) || !aligned16(p)) return S4R_ERR_INVALID_ARG;
+  if ((a->free_capacity > 0 && !a->free_pages) || !aligned16(a->free_pages)) return S4R_ERR_INVALID_ARG;
+  if ((a->max_tokens > 0 && !a->slots) || !aligned16(a->slots)) return S4R_ERR_INVALID_ARG;
+  const void *optional[] = {a->positions, a->requests, a->status_workspace};
+  for (const void *p : optional)
+    if (!aligned16(p)) return S4R_ERR_INVALID_ARG;
+  PagePlan p{a->batch, a->page_size, log2_of(a->page_size), a->max_pages, a->free_capacity, a->max_tokens,
+             a->lengths, a->new_tokens, a->free_pages, a->free_count, a->block_table, a->lengths_out,
+             a->free_count_out, a->cu_tokens, a->slots, a->positions, a->requests,
+             static_cast<uint32_t *>(a->status_workspace)};
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const size_t smem = plan_smem_bytes(a->batch);
+  if (ensure_smem<page_plan_kernel>(smem) != cudaSuccess || ensure_smem<page_commit_kernel>(smem) != cudaSuccess)
+    return fail("page_plan_kernel (shared memory)", cudaGetLastError());
+  const unsigned grid = grid_of(ceil_div(a->max_tokens, kPlanTokensPerCta), sm_count());
+  page_plan_kernel<<<grid, kPlanThreads, smem, st>>>(p);
+  if (grid > 1) page_commit_kernel<<<1, kPlanThreads, smem, st>>>(p);
+  return check_launch("page_plan_kernel");
+}
+
+s4r_status s4r_latent_write(const s4r_latent_write_args *a, void *stream) {
+  if (!a) return S4R_ERR_INVALID_ARG;
+  const s4r_status rc = cache_shape_ok(a->cache_dtype, a->width, a->page_size, a->n_pages, a->cache_scale);
+  if (rc != S4R_OK) return rc;
+  if (a->n_tokens < 0 || a->latents_ld < a->width) return S4R_ERR_INVALID_ARG;
+  if (a->n_tokens > INT32_MAX) return S4R_ERR_UNSUPPORTED;
+  if (a->n_tokens == 0) return S4R_OK;
+  if (!a->latents || !a->slots || (a->n_pages > 0 && !a->cache)) return S4R_ERR_INVALID_ARG;
+  const void *all[] = {a->latents, a->slots, a->cache, a->stored, a->status_workspace};
+  for (const void *p : all)
+    if (!aligned16(p)) return S4R_ERR_INVALID_ARG;
+  if (a->latents_ld % 8 || (a->stored && a->cache_dtype != S4R_FP4)) return S4R_ERR_INVALID_ARG;
+  LatentWrite p{a->n_tokens, a->n_pages * a->page_size, a->latents_ld, a->width, a->page_size, log2_of(a->page_size),
+                a->cache_scale, static_cast<const bf16 *>(a->latents), a->slots, static_cast<unsigned char *>(a->cache),
+                static_cast<bf16 *>(a->stored), static_cast<uint32_t *>(a->status_workspace)};
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const int64_t items = a->n_tokens * (a->width / (a->cache_dtype == S4R_FP4 ? 16 : 8));
+  const unsigned grid = grid_of(ceil_div(items, 256), 16 * sm_count());
+  if (a->cache_dtype == S4R_FP4) latent_write_fp4<<<grid, 256, 0, st>>>(p);
+  else latent_write_bf16<<<grid, 256, 0, st>>>(p);
+  return check_launch("latent_write");
+}
+
+size_t s4r_latent_attend_workspace_bytes(const s4r_latent_attend_args *a) {
+  return latent_attend_shape(a) == S4R_OK ? latent_attend_bytes(a) : 0;
+}
+
+s4r_status s4r_latent_attend(const s4r_latent_attend_args *a, void *stream) {
+  const s4r_status rc = latent_attend_shape(a);
+  if (rc != S4R_OK) return rc;
+  if (a->batch == 0) return S4R_OK;
+  const void *must[] = {a->q, a->block_table, a->lengths, a->out};
+  for (const void *p : must)
+    if (!p || !aligned16(p)) return S4R_ERR_INVALID_ARG;
+  if ((a->n_pages > 0 && !a->cache) || !aligned16(a->cache) || !aligned16(a->lse)) return S4R_ERR_INVALID_ARG;
+  if (!a->workspace || !aligned16(a->workspace) || a->workspace_bytes < latent_attend_bytes(a)) return S4R_ERR_WORKSPACE;
+  LatentAttend p{a->batch, a->n_query, a->n_heads, a->width, a->rank, a->page_size, log2_of(a->page_size), a->max_pages,
+                 a->n_pages, a->scale, a->cache_dtype == S4R_FP4 ? a->cache_scale : 1.0f, static_cast<const bf16 *>(a->q),
+                 static_cast<const unsigned char *>(a->cache), a->block_table, a->lengths, static_cast<bf16 *>(a->out),
+                 a->lse, static_cast<uint32_t *>(a->workspace)};
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const unsigned grid = (unsigned)ceil_div((int64_t)a->batch * a->n_query * a->n_heads, 8);
+  if (a->cache_dtype == S4R_FP4) latent_attend_simt<true><<<grid, 256, 0, st>>>(p);
+  else latent_attend_simt<false><<<grid, 256, 0, st>>>(p);
+  return check_launch("latent_attend");
+}
+
+s4r_status s4r_latent_project(const s4r_latent_project_args *a, void *stream) {
+  if (!a) return S4R_ERR_INVALID_ARG;
+  if (a->n_tokens < 0 || a->n_heads <= 0 || a->head_dim <= 0 || a->rank <= 0) return S4R_ERR_INVALID_ARG;
+  if (a->head_dim % 8 || a->rank % 8 || a->head_dim > S4R_MAX_HEAD_DIM || a->rank > S4R_MAX_LATENT_RANK ||
+      a->n_tokens > INT32_MAX || a->n_heads > 65535)
+    return S4R_ERR_UNSUPPORTED;
+  if (a->n_tokens == 0) return S4R_OK;
+  const int64_t n_in = a->to_latent ? a->head_dim : a->rank, n_out = a->to_latent ? a->rank : a->head_dim;
+  if (!a->x || !a->basis || !a->out || !aligned16(a->x) || !aligned16(a->basis) || !aligned16(a->out))
+    return S4R_ERR_INVALID_ARG;
+  if (a->x_ts % 8 || a->x_hs % 8 || a->out_ts % 8 || a->out_hs % 8) return S4R_ERR_INVALID_ARG;
+  // Either stride may be the outer one; an input may repeat its row for every
+  // head, an output row may not touch another.
+  auto apart = [&](int64_t ts, int64_t hs, int64_t n) {
+    const bool one_t = a->n_tokens == 1, one_h = a->n_heads == 1;
+    if ((!one_t && ts < n) || (!one_h && hs < n)) return false;
+    if (one_t || one_h) return true;
+    return ts >= hs * (a->n_heads - 1) + n || hs >= ts * (a->n_tokens - 1) + n;
+  };
+  if (a->x_ts < 0 || a->x_hs < 0 || a->out_ts < 0 || a->out_hs < 0) return S4R_ERR_INVALID_ARG;
+  if ((a->n_tokens > 1 && a->x_ts < n_in) || (a->x_hs != 0 && a->x_hs < n_in) || !apart(a->out_ts, a->out_hs, n_out))
+    return S4R_ERR_INVALID_ARG;
+  LatentProject p{a->n_tokens, a->n_heads, a->head_dim, a->rank, a->to_latent, static_cast<const bf16 *>(a->x),
+                  static_cast<const bf16 *>(a->basis), static_cast<bf16 *>(a->out), a->x_ts, a->x_hs, a->out_ts, a->out_hs};
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  latent_project_simt<<<grid_of(ceil_div(a->n_tokens * a->n_heads * n_out, 256), 64 * sm_count()), 256, 0, st>>>(p);
+  return check_launch("latent_project");
+}
+
+s4r_status s4r_prefill_attend(const s4r_prefill_attend_args *a, void *stream) {
+  if (!a) return S4R_ERR_INVALID_ARG;
+  if (a->batch < 0 || a->n_heads_q <= 0 || a->n_heads_kv <= 0 || a->head_dim <= 0 || a->rope_dim < 0 ||
+      a->value_dim <= 0 || a->max_q < 0 || a->total_q < 0 || a->total_k < 0 || !std::isfinite(a->scale) ||
+      a->n_heads_q % a->n_heads_kv)
+    return S4R_ERR_INVALID_ARG;
+  if (a->head_dim % 8 || a->rope_dim % 8 || a->value_dim % 8 || a->head_dim > 128 || a->value_dim > 128 ||
+      a->rope_dim > 64 || a->batch > 65535 || a->n_heads_q > 65535 || a->total_q > INT32_MAX || a->total_k > INT32_MAX)
+    return S4R_ERR_UNSUPPORTED;
+  if (a->batch == 0 || a->total_q == 0 || a->max_q == 0) return S4R_OK;
+  const void *must[] = {a->q, a->cu_q, a->cu_k, a->out};
+  for (const void *p : must)
+    if (!p || !aligned16(p)) return S4R_ERR_INVALID_ARG;
+  const bool keys = a->total_k > 0;
+  if ((keys && (!a->k || !a->v || (a->rope_dim > 0 && !a->k_rope))) || !aligned16(a->k) || !aligned16(a->v) ||
+      !aligned16(a->k_rope) || !aligned16(a->lse))
+    return S4R_ERR_INVALID_ARG;
+  if (a->k_ts % 8 || a->v_ts % 8 || a->k_rope_ts % 8) return S4R_ERR_INVALID_ARG;
+  if (keys && (a->k_ts < (int64_t)a->n_heads_kv * a->head_dim || a->v_ts < (int64_t)a->n_heads_kv * a->value_dim ||
+               (a->rope_dim > 0 && a->k_rope_ts < a->rope_dim)))
+    return S4R_ERR_INVALID_ARG;
+  PrefillAttend p{a->batch, a->n_heads_q, a->n_heads_kv, a->head_dim, a->rope_dim, a->value_dim, a->causal, a->max_q,
+                  a->total_q, a->total_k, a->scale, static_cast<const bf16 *>(a->q), static_cast<const bf16 *>(a->k),
+                  static_cast<const bf16 *>(a->v), static_cast<const bf16 *>(a->k_rope), a->k_ts, a->v_ts, a->k_rope_ts,
+                  a->cu_q, a->cu_k, static_cast<bf16 *>(a->out), a->lse};
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  prefill_attend_simt<<<dim3((unsigned)ceil_div(a->max_q, 8), (unsigned)a->n_heads_q, (unsigned)a->batch), 256, 0, st>>>(p);
+  return check_launch("prefill_attend");
+}
+
+}  // extern "C"

@@ -20,6 +20,10 @@
 #include "k_basis.cuh"
 #include "k_encode_simt.cuh"
 #include "k_encode_tc.cuh"
+#include "k_latent.cuh"
+#include "k_latent_project.cuh"
+#include "k_page.cuh"
+#include "k_prefill.cuh"
 #include "k_project.cuh"
 #include "k_score_simt.cuh"
 #include "k_score_pair.cuh"
@@ -1123,3 +1127,5 @@ extern "C" s4r_status s4r_decode_step_noalloc(const s4r_decode_args *a, void *st
   noalloc_fold_status<<<1, 1, 0, st>>>(reinterpret_cast<uint32_t *>(static_cast<unsigned char *>(scratch) + ly.status));
   return check_launch("noalloc_fold_status");
 }
+
+#include "api_latent.cuh"
