@@ -407,7 +407,7 @@ s4r_status s4r_latent_write(const s4r_latent_write_args *args, void *stream);
  * product only.
  * Device status (S4R_ERR_DEVICE): a length outside [0, max_pages *
  * page_size] (clamped), a page id outside [0, n_pages) among a request's
- * pages (its rows read as zeros); S4R_ERR_TIMEOUT as elsewhere.  The outputs
+ * pages (not read); S4R_ERR_TIMEOUT as elsewhere.  The outputs
  * of such a request are not defined.
  * Workspace: s4r_latent_attend_workspace_bytes(args) bytes, prepared once
  * with s4r_workspace_init; calls that may overlap in time need their own. */
@@ -419,7 +419,7 @@ typedef struct {
   int32_t rank;              /* leading values that are attended; multiple of 8, <= width */
   int32_t page_size, max_pages;
   s4r_dtype cache_dtype;     /* S4R_BF16 or S4R_FP4 */
-  int64_t n_pages;
+  int64_t n_pages;           /* >= 1 */
   float scale;               /* of the logits */
   float cache_scale;         /* S4R_FP4: > 0; ignored for S4R_BF16 */
   const void *q;             /* [batch][n_query][n_heads][width] bf16 */

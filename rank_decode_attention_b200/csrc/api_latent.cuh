@@ -40,12 +40,82 @@ s4r_status latent_attend_shape(const s4r_latent_attend_args *a) {
     return S4R_ERR_INVALID_ARG;
   if (a->rank % 8 || a->rank > S4R_MAX_LATENT_RANK || a->batch > S4R_MAX_REQUESTS ||
       (int64_t)a->n_query * a->n_heads > INT32_MAX / S4R_MAX_LATENT_WIDTH ||
+      (int64_t)a->n_query * a->n_heads * a->batch > INT32_MAX ||
       (int64_t)a->max_pages * a->page_size > INT32_MAX)
     return S4R_ERR_UNSUPPORTED;
   return S4R_OK;
 }
 
-size_t latent_attend_bytes(const s4r_latent_attend_args *) { return kAlign; }
+// Blocks of query rows, grid and workspace of a latent attention call.
+struct LatentPlan {
+  int nb, row_blocks, n_ctas;
+  size_t flags, ml, part, total;
+};
+LatentPlan latent_plan(const s4r_latent_attend_args *a) {
+  LatentPlan l;
+  const int64_t rows = (int64_t)a->n_query * a->n_heads;
+  l.row_blocks = (int)ceil_div(rows, 64);
+  l.nb = la_block_rows(rows);
+  const int64_t tiles = (int64_t)a->batch * l.row_blocks * ceil_div((int64_t)a->max_pages * a->page_size, kLaTile);
+  l.n_ctas = (int)smax<int64_t>(1, smin<int64_t>(tiles, sm_count()));
+  size_t off = kAlign;   // status word
+  l.flags = off;
+  off += round_up(sizeof(int32_t) * (size_t)a->batch * l.row_blocks);
+  l.ml = off;
+  off += round_up(sizeof(float2) * 2 * (size_t)l.n_ctas * l.nb);
+  l.part = off;
+  off += round_up(sizeof(float) * 2 * (size_t)l.n_ctas * l.nb * a->rank);
+  l.total = off;
+  return l;
+}
+
+// bf16 tensor map of up to three dimensions (innermost first), 128-byte swizzle.
+bool make_tmap_bf16_nd(CUtensorMap *map, const void *ptr, int n, const uint64_t *dims, const uint64_t *stride_bytes,
+                       const uint32_t *box) {
+  auto fn = tensor_map_encoder();
+  if (!fn) return false;
+  cuuint64_t d[3], st[2];
+  cuuint32_t b[3], es[3] = {1, 1, 1};
+  for (int i = 0; i < n; ++i) {
+    d[i] = dims[i];
+    b[i] = box[i];
+    if (i + 1 < n) st[i] = stride_bytes[i];
+  }
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)n, const_cast<void *>(ptr), d, st, b, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int NB, bool FP4>
+s4r_status latent_attend_launch(const LatentAttend &p, cudaStream_t st) {
+  CUtensorMap kv{}, q{};
+  if (!FP4) {
+    const uint64_t row = (uint64_t)p.width * 2;
+    const uint64_t kd[3] = {(uint64_t)p.width, (uint64_t)p.page_size, (uint64_t)p.n_pages};
+    const uint64_t ks[2] = {row, row * p.page_size};
+    const uint32_t kb[3] = {64, (uint32_t)smin(p.page_size, kLaTile), 1};
+    const uint64_t qd[2] = {(uint64_t)p.width, (uint64_t)p.batch * p.rows};
+    const uint32_t qb[2] = {64, (uint32_t)NB};
+    if (!make_tmap_bf16_nd(&kv, p.cache, 3, kd, ks, kb) || !make_tmap_bf16_nd(&q, p.q, 2, qd, &row, qb)) {
+      snprintf(g_last_error, sizeof(g_last_error), "cuTensorMapEncodeTiled failed for the latent cache or the queries");
+      return S4R_ERR_CUDA;
+    }
+  }
+  const size_t smem = (size_t)la_layout(NB, p.width, FP4).total;
+  cudaError_t err = ensure_smem<latent_attend_kernel<NB, FP4>>(smem);
+  if (err != cudaSuccess) return fail("latent_attend_kernel (shared memory)", err);
+  latent_attend_kernel<NB, FP4><<<(unsigned)p.n_ctas, 192 + (FP4 ? kLaDequantWarps * 32 : 0), smem, st>>>(kv, q, p);
+  if (check_launch("latent_attend_kernel") != S4R_OK) return S4R_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((int64_t)p.batch * p.rows), (unsigned)ceil_div(p.rank, 128));
+  cfg.blockDim = dim3(kLcThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1] = {pdl_attr()};
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  err = cudaLaunchKernelEx(&cfg, latent_combine_kernel<NB, FP4>, p);
+  return err == cudaSuccess ? S4R_OK : fail("latent_combine_kernel", err);
+}
 
 }  // namespace
 
@@ -107,7 +177,7 @@ s4r_status s4r_latent_write(const s4r_latent_write_args *a, void *stream) {
 }
 
 size_t s4r_latent_attend_workspace_bytes(const s4r_latent_attend_args *a) {
-  return latent_attend_shape(a) == S4R_OK ? latent_attend_bytes(a) : 0;
+  return latent_attend_shape(a) == S4R_OK ? latent_plan(a).total : 0;
 }
 
 s4r_status s4r_latent_attend(const s4r_latent_attend_args *a, void *stream) {
@@ -117,17 +187,45 @@ s4r_status s4r_latent_attend(const s4r_latent_attend_args *a, void *stream) {
   const void *must[] = {a->q, a->block_table, a->lengths, a->out};
   for (const void *p : must)
     if (!p || !aligned16(p)) return S4R_ERR_INVALID_ARG;
-  if ((a->n_pages > 0 && !a->cache) || !aligned16(a->cache) || !aligned16(a->lse)) return S4R_ERR_INVALID_ARG;
-  if (!a->workspace || !aligned16(a->workspace) || a->workspace_bytes < latent_attend_bytes(a)) return S4R_ERR_WORKSPACE;
-  LatentAttend p{a->batch, a->n_query, a->n_heads, a->width, a->rank, a->page_size, log2_of(a->page_size), a->max_pages,
-                 a->n_pages, a->scale, a->cache_dtype == S4R_FP4 ? a->cache_scale : 1.0f, static_cast<const bf16 *>(a->q),
-                 static_cast<const unsigned char *>(a->cache), a->block_table, a->lengths, static_cast<bf16 *>(a->out),
-                 a->lse, static_cast<uint32_t *>(a->workspace)};
+  if (a->n_pages < 1 || !a->cache || !aligned16(a->cache) || !aligned16(a->lse)) return S4R_ERR_INVALID_ARG;
+  const LatentPlan l = latent_plan(a);
+  if (!a->workspace || !aligned16(a->workspace) || a->workspace_bytes < l.total) return S4R_ERR_WORKSPACE;
+  const bool fp4 = a->cache_dtype == S4R_FP4;
+  unsigned char *ws = static_cast<unsigned char *>(a->workspace);
+  LatentAttend p{};
+  p.batch = a->batch;
+  p.n_query = a->n_query;
+  p.n_heads = a->n_heads;
+  p.width = a->width;
+  p.rank = a->rank;
+  p.page_size = a->page_size;
+  p.page_shift = log2_of(a->page_size);
+  p.max_pages = a->max_pages;
+  p.n_pages = a->n_pages;
+  p.scale = a->scale;
+  p.cache_scale = fp4 ? a->cache_scale : 1.0f;
+  p.q = static_cast<const bf16 *>(a->q);
+  p.cache = static_cast<const unsigned char *>(a->cache);
+  p.block_table = a->block_table;
+  p.lengths = a->lengths;
+  p.out = static_cast<bf16 *>(a->out);
+  p.lse = a->lse;
+  p.rows = a->n_query * a->n_heads;
+  p.row_blocks = l.row_blocks;
+  p.n_ctas = l.n_ctas;
+  p.slots = la_layout(l.nb, a->width, fp4).slots;
+  p.status = reinterpret_cast<uint32_t *>(ws);
+  p.flags = reinterpret_cast<int32_t *>(ws + l.flags);
+  p.ml = reinterpret_cast<float2 *>(ws + l.ml);
+  p.part = reinterpret_cast<float *>(ws + l.part);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const unsigned grid = (unsigned)ceil_div((int64_t)a->batch * a->n_query * a->n_heads, 8);
-  if (a->cache_dtype == S4R_FP4) latent_attend_simt<true><<<grid, 256, 0, st>>>(p);
-  else latent_attend_simt<false><<<grid, 256, 0, st>>>(p);
-  return check_launch("latent_attend");
+  if (fp4)
+    return l.nb == 16   ? latent_attend_launch<16, true>(p, st)
+           : l.nb == 32 ? latent_attend_launch<32, true>(p, st)
+                        : latent_attend_launch<64, true>(p, st);
+  return l.nb == 16   ? latent_attend_launch<16, false>(p, st)
+         : l.nb == 32 ? latent_attend_launch<32, false>(p, st)
+                      : latent_attend_launch<64, false>(p, st);
 }
 
 s4r_status s4r_latent_project(const s4r_latent_project_args *a, void *stream) {

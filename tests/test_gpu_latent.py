@@ -332,6 +332,27 @@ def test_latent_attend_infinite_values_in_seen_rows(dt):
     assert_within(d["lse"][1, 0].cpu(), lse, lb)
 
 
+@pytest.mark.parametrize("H", [5, 40])
+@pytest.mark.parametrize("n", [3, 64, 66, 20000])
+def test_latent_attend_infinities_that_only_later_queries_see(n, H):
+    """The newest row holds an infinity and the one before it a NaN in a value column: the queries that do not see them
+    stay exact."""
+    p = latent_problem("bf16", [n, 100], 3, H, 192, 32, seed=n)
+    flat = p["cache"].view(-1, 192)
+    for back, bad in ((1, math.inf), (2, math.nan)):
+        at = n - back
+        flat[int(p["table"][0, at // 32]) * 32 + at % 32, 7 * back] = bad
+    d = run_latent(p, 160, 0.05)
+    assert d["status"] == s4r.S4R_OK
+    out, lse, ob, lb = latent_attend(p["q"][0, 0].double(), p["rows"][0], n - 2, 160, 0.05, 2.0 ** -8)
+    assert_within(d["out"][0, 0].cpu(), out, ob)
+    assert_within(d["lse"][0, 0].cpu(), lse, lb)
+    assert torch.isnan(d["out"][0, 1]).all() and torch.isnan(d["out"][0, 2]).all()
+    for t in range(3):
+        out, lse, ob, lb = latent_attend(p["q"][1, t].double(), p["rows"][1], 98 + t, 160, 0.05, 2.0 ** -8)
+        assert_within(d["out"][1, t].cpu(), out, ob)
+
+
 @pytest.mark.parametrize("dt", ["bf16", "fp4"])
 def test_latent_attend_reports_bad_lengths_and_pages(dt):
     p = latent_problem(dt, [100, 50, 20, 64], 1, 4, 64, 16, seed=10)
