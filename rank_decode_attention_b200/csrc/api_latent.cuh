@@ -49,7 +49,7 @@ s4r_status latent_attend_shape(const s4r_latent_attend_args *a) {
 // Blocks of query rows, grid and workspace of a latent attention call.
 struct LatentPlan {
   int nb, row_blocks, n_ctas;
-  size_t flags, ml, part, total;
+  size_t flags, units, ml, part, total;
 };
 LatentPlan latent_plan(const s4r_latent_attend_args *a) {
   LatentPlan l;
@@ -61,6 +61,8 @@ LatentPlan latent_plan(const s4r_latent_attend_args *a) {
   size_t off = kAlign;   // status word
   l.flags = off;
   off += round_up(sizeof(int32_t) * (size_t)a->batch * l.row_blocks);
+  l.units = off;
+  off += round_up(sizeof(int2) * (size_t)a->batch * l.row_blocks);
   l.ml = off;
   off += round_up(sizeof(float2) * 2 * (size_t)l.n_ctas * l.nb);
   l.part = off;
@@ -104,16 +106,19 @@ s4r_status latent_attend_launch(const LatentAttend &p, cudaStream_t st) {
   const size_t smem = (size_t)la_layout(NB, p.width, FP4).total;
   cudaError_t err = ensure_smem<latent_attend_kernel<NB, FP4>>(smem);
   if (err != cudaSuccess) return fail("latent_attend_kernel (shared memory)", err);
-  latent_attend_kernel<NB, FP4><<<(unsigned)p.n_ctas, 192 + (FP4 ? kLaDequantWarps * 32 : 0), smem, st>>>(kv, q, p);
+  latent_attend_kernel<NB, FP4><<<(unsigned)p.n_ctas, la_threads(FP4), smem, st>>>(kv, q, p);
   if (check_launch("latent_attend_kernel") != S4R_OK) return S4R_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((int64_t)p.batch * p.rows), (unsigned)ceil_div(p.rank, 128));
+  // Few rows with many parts each: their columns go to CTAs of their own.
+  const int64_t out_rows = (int64_t)p.batch * p.rows;
+  const int cols = out_rows < 2 * sm_count() ? 128 : (int)ceil_div(p.rank, 128) * 128;
+  cfg.gridDim = dim3((unsigned)out_rows, (unsigned)ceil_div(p.rank, cols));
   cfg.blockDim = dim3(kLcThreads);
   cfg.stream = st;
   cudaLaunchAttribute attr[1] = {pdl_attr()};
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  err = cudaLaunchKernelEx(&cfg, latent_combine_kernel<NB, FP4>, p);
+  err = cudaLaunchKernelEx(&cfg, latent_combine_kernel<NB, FP4>, p, cols);
   return err == cudaSuccess ? S4R_OK : fail("latent_combine_kernel", err);
 }
 
@@ -216,6 +221,7 @@ s4r_status s4r_latent_attend(const s4r_latent_attend_args *a, void *stream) {
   p.slots = la_layout(l.nb, a->width, fp4).slots;
   p.status = reinterpret_cast<uint32_t *>(ws);
   p.flags = reinterpret_cast<int32_t *>(ws + l.flags);
+  p.units = reinterpret_cast<int2 *>(ws + l.units);
   p.ml = reinterpret_cast<float2 *>(ws + l.ml);
   p.part = reinterpret_cast<float *>(ws + l.part);
   cudaStream_t st = static_cast<cudaStream_t>(stream);

@@ -28,11 +28,11 @@
 //              ring holds it, before O^T of tile i, so the softmax of one tile
 //              runs beside the products of another; slots are released column
 //              block by column block;
-//   warps 2-5  softmax: probabilities against a reference maximum that moves
+//   warps 2-9  softmax: probabilities against a reference maximum that moves
 //              only when a logit exceeds it by more than 2^8 (then O^T is
 //              rescaled in TMEM), sums in fp32, P^T into shared memory; at the
 //              end of a unit they write the result or the partial sums.
-//   warps 6-13 (4-bit cache) turn codes into fp16 ring slots: e2m1 * e4m3 has
+//   warps 10-17 (4-bit cache) turn codes into fp16 ring slots: e2m1 * e4m3 has
 //              6 significant bits, so fp16 holds the stored values exactly.
 //              Queries become fp16 too, scaled by a power of two per row, exact
 //              over 29 binades below the row's largest value.
@@ -56,7 +56,9 @@ constexpr int kLaSlot = kLaTile * 128 * 2;   // bytes of a ring slot: 64 tokens 
 constexpr int kLaMaxSlots = 12;
 constexpr int kLaMaxPairs = (S4R_MAX_LATENT_WIDTH + 127) / 128;
 constexpr int kLaSmemBudget = 227 * 1024;
-constexpr int kLaDequantWarps = 8;
+constexpr int kLaSoftmaxWarps = 8;           // two groups of 4, half of the query rows each
+constexpr int kLaDequantWarps = 8;           // groups of kLaDequantGroup take turns at the ring slots
+constexpr int kLaDequantGroup = 2;
 constexpr int kLaRawStages = 2;
 constexpr float kLaLift = 8.0f;              // how far (in powers of two) a logit may exceed the reference
 
@@ -74,6 +76,7 @@ struct LatentAttend {
   // workspace
   uint32_t *status;
   int32_t *flags;                            // [batch * row_blocks] recompute the unit (see latent_combine_kernel)
+  int2 *units;                               // [batch * row_blocks] first part, and how many (1: computed whole)
   float2 *ml;                                // [2 * n_ctas][NB] reference maximum and sum of a partial
   float *part;                               // [2 * n_ctas][NB][rank] unscaled partial results
 };
@@ -81,10 +84,12 @@ struct LatentAttend {
 // Query rows a block of the kernel takes, and how many blocks a request has.
 __host__ __device__ inline int la_block_rows(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
 
+__host__ __device__ constexpr int la_threads(bool fp4) { return 64 + 32 * (kLaSoftmaxWarps + (fp4 ? kLaDequantWarps : 0)); }
+
 struct LaLayout {
   int q, p, raw, ring, control, total, slots;
 };
-constexpr int kLaControlBytes = 4096;
+constexpr int kLaControlBytes = 2048;
 __host__ __device__ inline int la_raw_bytes(int width) { return (kLaTile * width * 9 / 16 + 127) / 128 * 128; }
 __host__ __device__ inline LaLayout la_layout(int nb, int width, bool fp4) {
   LaLayout l;
@@ -94,7 +99,7 @@ __host__ __device__ inline LaLayout la_layout(int nb, int width, bool fp4) {
   off += chunks * nb * 128;
   off = (off + 1023) & ~1023;
   l.p = off;
-  off += 2 * kLaTile * 128;
+  off += kLaTile * 128;
   l.ring = off;
   const int tail = (fp4 ? kLaRawStages * la_raw_bytes(width) : 0) + kLaControlBytes + 1024;
   l.slots = smin((kLaSmemBudget - off - tail) / kLaSlot, kLaMaxSlots);
@@ -110,12 +115,13 @@ __host__ __device__ inline LaLayout la_layout(int nb, int width, bool fp4) {
 struct LaControl {
   uint64_t full[kLaMaxSlots], empty[kLaMaxSlots];
   uint64_t raw_full[kLaRawStages], raw_empty[kLaRawStages];
-  uint64_t s_full[2], p_full[2], pv_done[2];
+  uint64_t s_full[2], p_full, pv_done;
   uint64_t q_full, q_empty, o_free;
   uint32_t tmem_base;
   int fail;   // a wait of the softmax warps gave up
   int first_b, first_off, n_tiles;   // start of this CTA's range and its length
-  int qexp[2][64];                   // 4-bit cache: queries are scaled by 2^qexp (segments alternate)
+  int share;                         // tiles of a full range
+  int16_t qexp[2][64];               // 4-bit cache: queries are scaled by 2^qexp (segments alternate)
   alignas(8) float wmax[4][64];
   float fac[64];
 };
@@ -129,35 +135,21 @@ __device__ __forceinline__ int32_t la_length(const LatentAttend &p, int b) {
 }
 __device__ __forceinline__ int32_t la_tiles(int32_t len) { return (len + kLaTile - 1) / kLaTile; }
 
-// Tiles of all units of the batch, those of requests before `upto` (both
-// block-wide results in every thread).  scratch: blockDim.x / 32 pairs.
-__device__ inline void la_count(const LatentAttend &p, int upto, long long *scratch, long long &total, long long &before) {
-  long long t = 0, f = 0;
-  for (int b = threadIdx.x; b < p.batch; b += blockDim.x) {
-    const long long n = (long long)la_tiles(la_length(p, b)) * p.row_blocks;
-    t += n;
-    if (b < upto) f += n;
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    t += __shfl_xor_sync(0xffffffffu, t, o);
-    f += __shfl_xor_sync(0xffffffffu, f, o);
-  }
-  const int warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-  if ((threadIdx.x & 31) == 0) {
-    scratch[2 * warp] = t;
-    scratch[2 * warp + 1] = f;
-  }
-  __syncthreads();
-  total = before = 0;
-  for (int w = 0; w < nw; ++w) {
-    total += scratch[2 * w];
-    before += scratch[2 * w + 1];
-  }
-  __syncthreads();
-}
 // Tiles a CTA takes of `total`.
 __host__ __device__ inline long long la_share(long long total, int n_ctas) { return (total + n_ctas - 1) / n_ctas; }
+
+// A place in a ring of n slots and the parity of its turn (no divisions: the
+// single-warp roles are bound by the instructions they issue).
+struct LaRing {
+  int st = 0;
+  uint32_t turn = 0;
+  __device__ __forceinline__ void step(int n) {
+    if (++st == n) {
+      st = 0;
+      ++turn;
+    }
+  }
+};
 
 // The segments of a CTA: consecutive tiles of one unit.
 struct LaSegment {
@@ -194,71 +186,115 @@ struct LaWalk {
 // and lane t / 4 + 8 of the same columns in r[4j+2], r[4j+3].
 template <int N>
 __device__ __forceinline__ void tmem_ld16x256(uint32_t taddr, uint32_t (&r)[4 * N]) {
-  if constexpr (N == 2) {
+  if constexpr (N == 1) {
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(taddr));
+  } else if constexpr (N == 2) {
     asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                  : "r"(taddr));
-  } else if constexpr (N == 4) {
+  } else {
+    static_assert(N == 4, "groups of 8 columns");
     asm volatile(
         "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
           "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
         : "r"(taddr));
-  } else {
-    static_assert(N == 8, "groups of 8 columns");
-    asm volatile(
-        "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
-          "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
-          "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
-          "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(taddr));
   }
 }
-// 32 lanes x 16 columns (tmem_ld32 and tmem_st32 for half the columns).
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr));
+// 32 lanes x 8 columns (tmem_ld32 and tmem_st32 for a quarter of the columns).
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
 }
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(
-          taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+
+// tcgen05.mma and tcgen05.commit under a predicate.
+__device__ __forceinline__ void umma_f16_if(uint32_t on, uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                            bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"((uint32_t)accumulate), "r"(on)
+      : "memory");
+}
+__device__ __forceinline__ void umma_commit_if(uint32_t on, uint64_t *bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+      "r"(on)
       : "memory");
 }
 
-// Barrier of the 128 softmax threads, and the same with an "any" of a flag.
-__device__ __forceinline__ void la_bar() {
+// Barrier of a group of 128 softmax threads, and the same with an "any" of a flag.
+__device__ __forceinline__ void la_bar(int id) {
   __syncwarp();
-  asm volatile("barrier.cta.sync.aligned 1, 128;" ::: "memory");
+  asm volatile("barrier.cta.sync.aligned %0, 128;" ::"r"(id) : "memory");
 }
-__device__ __forceinline__ bool la_bar_any(bool x) {
+__device__ __forceinline__ bool la_bar_any(int id, bool x) {
   uint32_t r;
   __syncwarp();
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.u32 p, %1, 0;\n\t"
-      "barrier.cta.red.or.pred.aligned q, 1, 128, p;\n\t"
+      "barrier.cta.red.or.pred.aligned q, %2, 128, p;\n\t"
       "selp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
-      : "r"((uint32_t)x)
+      : "r"((uint32_t)x), "r"(id)
       : "memory");
   return r != 0;
 }
-// 3-D tiled load: columns, row in the page, page.
-__device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, uint64_t *bar, int32_t c0, int32_t c1, int32_t c2) {
+// Copies and barrier arrivals under a predicate, so that a warp stays in step
+// while one of its lanes issues.
+__device__ __forceinline__ void mbar_expect_if(uint32_t on, uint64_t *bar, uint32_t bytes) {
   asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+      "@q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(smem_u32(bar)),
+      "r"(bytes), "r"(on)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_2d_if(uint32_t on, void *dst, const CUtensorMap *map, uint64_t *bar, int32_t c0, int32_t c1) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];\n\t}" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(on)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_3d_if(uint32_t on, void *dst, const CUtensorMap *map, uint64_t *bar, int32_t c0, int32_t c1,
+                                               int32_t c2) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %6, 0;\n\t"
+      "@q cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];\n\t}" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(on)
+      : "memory");
+}
+__device__ __forceinline__ void bulk_load_if(uint32_t on, void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %4, 0;\n\t"
+      "@q cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n\t}" ::"r"(smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar)), "r"(on)
       : "memory");
 }
 // kind::f16 with fp16 operands instead of bf16 ones.
@@ -286,7 +322,7 @@ __device__ __forceinline__ bool la_not_finite(const uint4 &v) {
 }
 
 template <int NB, bool FP4>
-__global__ void __launch_bounds__(192 + (FP4 ? kLaDequantWarps * 32 : 0), 1)
+__global__ void __launch_bounds__(la_threads(FP4), 1)
 latent_attend_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant__ CUtensorMap map_q,
                      const LatentAttend p) {
   extern __shared__ __align__(1024) unsigned char la_smem_raw[];
@@ -294,28 +330,27 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_co
       (reinterpret_cast<uintptr_t>(la_smem_raw) + 1023) & ~uintptr_t(1023));
   const LaLayout ly = la_layout(NB, p.width, FP4);
   LaControl *ctl = reinterpret_cast<LaControl *>(smem + ly.control);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int chunks = (p.width + 63) / 64, pairs = (chunks + 1) / 2, vblocks = (p.rank + 127) / 128;
   const int n_slots = p.slots;
+  const long long limit = wait_limit();
   constexpr int kStatCols = 4 * NB;   // S^T behind the four blocks of O^T
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < n_slots; ++s) {
-      mbar_init(&ctl->full[s], FP4 ? kLaDequantWarps : 1);
+      mbar_init(&ctl->full[s], FP4 ? kLaDequantGroup : 1);
       mbar_init(&ctl->empty[s], 1);
     }
     for (int s = 0; s < kLaRawStages; ++s) {
       mbar_init(&ctl->raw_full[s], 1);
       mbar_init(&ctl->raw_empty[s], kLaDequantWarps);
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&ctl->s_full[i], 1);
-      mbar_init(&ctl->p_full[i], 4);
-      mbar_init(&ctl->pv_done[i], 1);
-    }
+    for (int i = 0; i < 2; ++i) mbar_init(&ctl->s_full[i], 1);
+    mbar_init(&ctl->p_full, kLaSoftmaxWarps);
+    mbar_init(&ctl->pv_done, 1);
     mbar_init(&ctl->q_full, FP4 ? kLaDequantWarps : 1);
     mbar_init(&ctl->q_empty, 1);
-    mbar_init(&ctl->o_free, 4);
+    mbar_init(&ctl->o_free, kLaSoftmaxWarps);
     mbar_fence_init();
     ctl->fail = 0;
     ctl->first_b = 0;
@@ -362,192 +397,223 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_co
       ctl->first_b = b;
       ctl->first_off = (int)(start - at);
       ctl->n_tiles = (int)smin<long long>(share, total - start);
+      ctl->share = (int)share;
     }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   pdl_trigger();   // the combine kernel may set itself up
-  const uint32_t tmem = ctl->tmem_base;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, ctl->tmem_base, 0);
   unsigned char *ring = smem + ly.ring;
 
-  if (threadIdx.x == 0) {
+  if (warp == 0) {
     // ------------------------------------------------------------ producer
+    // The whole warp in step, as in the MMA issuer below: its lanes read 32
+    // boxes' page ids at a time, one lane issues.
     LaWalk walk(ctl);
     LaSegment s;
-    uint32_t slot = 0, raw = 0;
+    LaRing slot, raw;
     bool ok = true;
-    const int box = smin(p.page_size, kLaTile);
-    while (ok && walk.next(p, s)) {
-      if constexpr (!FP4) {
-        if (s.index > 0) ok = mbar_wait(&ctl->q_empty, (uint32_t)(s.index - 1) & 1, p.status);
-        if (!ok) break;
-        mbar_arrive_expect_tx(&ctl->q_full, (uint32_t)(chunks * NB * 128));
-        for (int c = 0; c < chunks; ++c)
-          tma_load_2d(smem + ly.q + c * NB * 128, &map_q, &ctl->q_full, c * 64, s.b * p.rows + s.rb * NB);
-      }
+    const uint32_t leader = elect_one();
+    const int box = smin(p.page_size, kLaTile), box_shift = smin(p.page_shift, 6), per_tile = kLaTile >> box_shift;
+    const int64_t page_bytes = latent_page_bytes(true, p.page_size, p.width);
+    auto wait = [&](uint64_t *bar, uint32_t parity) {
+      return __shfl_sync(0xffffffffu, (int)mbar_wait_within(bar, parity & 1, limit, p.status), 0) != 0;
+    };
+    while (ok && __shfl_sync(0xffffffffu, (int)walk.next(p, s), 0)) {
+      s.b = __shfl_sync(0xffffffffu, s.b, 0);
+      s.rb = __shfl_sync(0xffffffffu, s.rb, 0);
+      s.tile = __shfl_sync(0xffffffffu, s.tile, 0);
+      s.n = __shfl_sync(0xffffffffu, s.n, 0);
+      s.len = __shfl_sync(0xffffffffu, s.len, 0);
+      s.index = __shfl_sync(0xffffffffu, s.index, 0);
+      // ids of the boxes from `first` on; a box behind the length has none
       const int32_t *table = p.block_table + (int64_t)s.b * p.max_pages;
-      int32_t id[4], next_id[4];
-      // pages of tile j: those that hold tokens below the length
-      auto look = [&](int j, int32_t (&to)[4]) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int64_t tok = (int64_t)j * kLaTile + i * box;
-          to[i] = (i * box < kLaTile && tok < s.len) ? table[tok >> p.page_shift] : 0;
-        }
-      };
-      look(s.tile, next_id);
-      for (int j = s.tile; j < s.tile + s.n && ok; ++j) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) id[i] = next_id[i];
-        if (j + 1 < s.tile + s.n) look(j + 1, next_id);
-        int boxes = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (i * box < kLaTile && j * kLaTile + i * box < s.len) {
-            boxes = i + 1;
-            if (id[i] < 0 || id[i] >= p.n_pages) set_status(p.status, kDevStatusCheck);
+      auto look = [&](int first) {
+        const int64_t tok = ((int64_t)first + lane) << box_shift;
+        int32_t id = 0;
+        if (tok < s.len) {
+          id = table[tok >> p.page_shift];
+          if (id < 0 || id >= p.n_pages) {
+            set_status(p.status, kDevStatusCheck);
+            id = -1;
           }
+        }
+        return id;
+      };
+      int next = s.tile * per_tile, left = 0;   // the box after those in `ids`; how many of `ids` are left
+      int32_t ids = 0, more = look(next);
+      if constexpr (!FP4) {
+        if (s.index > 0) ok = wait(&ctl->q_empty, (uint32_t)(s.index - 1));
+        if (!ok) break;
+        mbar_expect_if(leader, &ctl->q_full, (uint32_t)(chunks * NB * 128));
+        for (int c = 0; c < chunks; ++c)
+          tma_load_2d_if(leader, smem + ly.q + c * NB * 128, &map_q, &ctl->q_full, c * 64, s.b * p.rows + s.rb * NB);
+      }
+      for (int j = s.tile; j < s.tile + s.n && ok; ++j) {
+        if (left == 0) {   // 32 is a multiple of a tile's boxes
+          ids = more;
+          next += 32;
+          left = 32;
+          more = look(next);
+        }
+        const int at = 32 - left;
+        left -= per_tile;
+        const int boxes = smin(per_tile, (s.len - j * kLaTile + box - 1) >> box_shift);
         const int row = (j * kLaTile) & (p.page_size - 1);
         if constexpr (FP4) {
-          const int st = (int)(raw % kLaRawStages);
-          if (raw >= kLaRawStages) ok = mbar_wait(&ctl->raw_empty[st], ((raw / kLaRawStages) - 1) & 1, p.status);
+          const int st = raw.st;
+          if (raw.turn > 0) ok = wait(&ctl->raw_empty[st], raw.turn - 1);
           if (!ok) break;
           unsigned char *dst = smem + ly.raw + st * la_raw_bytes(p.width);
-          const int64_t page_bytes = latent_page_bytes(true, p.page_size, p.width);
           const uint32_t cb = (uint32_t)(box * (p.width / 2)), sb = (uint32_t)(box * (p.width / 16));
-          uint32_t bytes = 0;
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (i < boxes && id[i] >= 0 && id[i] < p.n_pages) bytes += cb + sb;
-          mbar_arrive_expect_tx(&ctl->raw_full[st], bytes);
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (i < boxes && id[i] >= 0 && id[i] < p.n_pages) {
-              const unsigned char *page = p.cache + id[i] * page_bytes;
-              bulk_load(dst + i * cb, page + (int64_t)row * (p.width / 2), cb, &ctl->raw_full[st]);
-              bulk_load(dst + kLaTile * (p.width / 2) + i * sb,
-                        page + (int64_t)p.page_size * (p.width / 2) + (int64_t)row * (p.width / 16), sb,
-                        &ctl->raw_full[st]);
-            }
-          ++raw;
+          const uint32_t known = __ballot_sync(0xffffffffu, ids >= 0) >> at;
+          mbar_expect_if(leader, &ctl->raw_full[st], (cb + sb) * __popc(known & ((1u << boxes) - 1u)));
+          for (int i = 0; i < boxes; ++i) {
+            const int32_t id = __shfl_sync(0xffffffffu, ids, at + i);
+            const unsigned char *page = p.cache + id * page_bytes;
+            const uint32_t on = leader && id >= 0;
+            bulk_load_if(on, dst + i * cb, page + (int64_t)row * (p.width / 2), cb, &ctl->raw_full[st]);
+            bulk_load_if(on, dst + kLaTile * (p.width / 2) + i * sb,
+                         page + (int64_t)p.page_size * (p.width / 2) + (int64_t)row * (p.width / 16), sb, &ctl->raw_full[st]);
+          }
+          raw.step(kLaRawStages);
         } else {
-          for (int k = 0; k < pairs && ok; ++k, ++slot) {
-            const int pr = pairs - 1 - k, st = (int)(slot % n_slots);
-            if (slot >= (uint32_t)n_slots) ok = mbar_wait(&ctl->empty[st], ((slot / n_slots) - 1) & 1, p.status);
+          for (int pr = pairs - 1; pr >= 0 && ok; --pr, slot.step(n_slots)) {
+            if (slot.turn > 0) ok = wait(&ctl->empty[slot.st], slot.turn - 1);
             if (!ok) break;
             const int halves = smin(2, chunks - 2 * pr);
-            unsigned char *dst = ring + st * kLaSlot;
-            mbar_arrive_expect_tx(&ctl->full[st], (uint32_t)(halves * boxes * box * 128));
-            for (int h = 0; h < halves; ++h)
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                if (i < boxes)
-                  tma_load_3d(dst + h * (kLaTile * 128) + i * box * 128, &map_kv, &ctl->full[st], (2 * pr + h) * 64, row, id[i]);
+            unsigned char *dst = ring + slot.st * kLaSlot;
+            mbar_expect_if(leader, &ctl->full[slot.st], (uint32_t)(halves * boxes) << (7 + box_shift));
+            for (int i = 0; i < boxes; ++i) {
+              // an unknown page is read as page -1: the copy fills in zeros
+              const int32_t id = __shfl_sync(0xffffffffu, ids, at + i);
+              tma_load_3d_if(leader, dst + (i << (7 + box_shift)), &map_kv, &ctl->full[slot.st], 2 * pr * 64, row, id);
+              if (halves > 1)
+                tma_load_3d_if(leader, dst + kLaTile * 128 + (i << (7 + box_shift)), &map_kv, &ctl->full[slot.st],
+                               (2 * pr + 1) * 64, row, id);
+            }
           }
         }
       }
     }
     if (!ok) {   // let the copies in flight land before the CTA ends
-      if constexpr (!FP4)
-        for (uint32_t n = slot > (uint32_t)n_slots ? slot - n_slots : 0; n < slot; ++n)
-          mbar_wait(&ctl->full[n % n_slots], (n / n_slots) & 1, p.status);
-      else
-        for (uint32_t n = raw > kLaRawStages ? raw - kLaRawStages : 0; n < raw; ++n)
-          mbar_wait(&ctl->raw_full[n % kLaRawStages], (n / kLaRawStages) & 1, p.status);
+      if constexpr (!FP4) {
+        for (int i = 0; i < n_slots; ++i)
+          if (slot.turn > 0 || i < slot.st) wait(&ctl->full[i], slot.turn - (i < slot.st ? 0 : 1));
+      } else {
+        for (int i = 0; i < kLaRawStages; ++i)
+          if (raw.turn > 0 || i < raw.st) wait(&ctl->raw_full[i], raw.turn - (i < raw.st ? 0 : 1));
+      }
     }
-  } else if (threadIdx.x == 32) {
+  } else if (warp == 1) {
     // ---------------------------------------------------------- MMA issuer
+    // The whole warp walks along and one lane issues under a predicate.  What
+    // steers it is broadcast from lane 0, so that the compiler sees uniform
+    // control flow and keeps descriptors in uniform registers: moving them
+    // there for every instruction took 70 cycles each, twice the 33 to 49 of
+    // the products themselves.
     LaWalk walk(ctl);
     LaSegment s;
     bool ok = true;
+    const uint32_t leader = elect_one();
     const uint32_t id_s = FP4 ? idesc_f16_f32(64, NB, 0, 0) : idesc_bf16_f32(64, NB, 0, 0);
     const uint32_t id_o = FP4 ? idesc_f16_f32(128, NB, 1, 1) : idesc_bf16_f32(128, NB, 1, 1);
-    uint32_t slot = 0, n = 0;   // ring slots and tiles so far
-    // the tile whose second product is still to be issued
-    bool due = false, due_first = false;
-    uint32_t due_slot = 0;
+    // descriptors of slot 0, of the queries' columns 0 and of P^T; the others are offsets (in 16 bytes) away
+    const uint64_t k_desc = sdesc_sw128(smem_u32(ring), 16, 1024), q_desc = sdesc_sw128(smem_u32(smem + ly.q), 16, 1024);
+    const uint64_t v_desc = sdesc_sw128(smem_u32(ring), kLaTile * 128, 1024);
+    const uint64_t p_desc = sdesc_sw128(smem_u32(smem + ly.p), kLaTile * 128, 1024);
+    auto wait = [&](uint64_t *bar, uint32_t parity) { return __shfl_sync(0xffffffffu, (int)mbar_wait_within(bar, parity & 1, limit, p.status), 0) != 0; };
+    LaRing slot;
+    uint32_t n = 0;                      // tiles so far
+    bool due = false, due_first = false; // the tile before waits for its second product; it is its unit's first
+    LaRing due_slot;                     // its first slot of values
     int due_index = 0;
     auto second = [&]() {   // O^T += V^T P^T of tile n - 1
-      const uint32_t t = n - 1, buf = t & 1;
-      if (!mbar_wait(&ctl->p_full[buf], (t >> 1) & 1, p.status)) return false;
-      if (due_first && due_index > 0 && !mbar_wait(&ctl->o_free, (uint32_t)(due_index - 1) & 1, p.status)) return false;
+      if (!wait(&ctl->p_full, n - 1)) return false;
+      if (due_first && due_index > 0 && !wait(&ctl->o_free, (uint32_t)(due_index - 1))) return false;
       tc_fence_after();
-      const uint32_t p_base = smem_u32(smem + ly.p + buf * (kLaTile * 128));
-      for (int k = pairs - vblocks; k < pairs; ++k) {
-        const int vb = pairs - 1 - k;
-        const int st = (int)((due_slot + k) % n_slots);
-        const uint32_t a_base = smem_u32(ring + st * kLaSlot);
+      for (int vb = vblocks - 1; vb >= 0; --vb, due_slot.step(n_slots)) {
+        const uint64_t a = v_desc + (uint32_t)due_slot.st * (kLaSlot >> 4);
 #pragma unroll
         for (int ks = 0; ks < kLaTile / 16; ++ks)
-          umma_f16(tmem + vb * NB, sdesc_sw128(a_base + ks * 2048, kLaTile * 128, 1024),
-                   sdesc_sw128(p_base + ks * 2048, kLaTile * 128, 1024), id_o, (due_first && ks == 0) ? 0u : 1u);
-        umma_commit(&ctl->empty[st]);
+          umma_f16_if(leader, tmem + vb * NB, a + ks * (2048 >> 4), p_desc + ks * (2048 >> 4), id_o, ks > 0 || !due_first);
+        umma_commit_if(leader, &ctl->empty[due_slot.st]);
       }
-      umma_commit(&ctl->pv_done[buf]);
+      umma_commit_if(leader, &ctl->pv_done);
       return true;
     };
-    while (ok && walk.next(p, s)) {
+    while (ok && __shfl_sync(0xffffffffu, (int)walk.next(p, s), 0)) {
+      s.n = __shfl_sync(0xffffffffu, s.n, 0);
+      s.index = __shfl_sync(0xffffffffu, s.index, 0);
       // between units the queries change: finish the last one while they load
       if (due) ok = second();
       due = false;
-      if (ok) ok = mbar_wait(&ctl->q_full, (uint32_t)s.index & 1, p.status);
+      if (ok) ok = wait(&ctl->q_full, (uint32_t)s.index);
       for (int j = 0; j < s.n && ok; ++j) {
         const uint32_t d = tmem + kStatCols + (n & 1) * NB;
-        const uint32_t my_slot = slot;
-        for (int k = 0; k < pairs && ok; ++k, ++slot) {
-          const int pr = pairs - 1 - k, st = (int)(slot % n_slots);
+        LaRing first = slot;
+        for (int k = pairs - 1; k >= 0 && ok; --k, slot.step(n_slots)) {
           // a slot that the tile before still holds comes free with its second product
-          if (due && slot >= (uint32_t)n_slots && slot - n_slots >= due_slot + (uint32_t)(pairs - vblocks)) {
+          if (due && slot.turn > 0 && (slot.turn - 1 > due_slot.turn || (slot.turn - 1 == due_slot.turn && slot.st >= due_slot.st))) {
             ok = second();
             due = false;
           }
-          if (ok) ok = mbar_wait(&ctl->full[st], (slot / n_slots) & 1, p.status);
+          if (ok) ok = wait(&ctl->full[slot.st], slot.turn);
           if (!ok) break;
           tc_fence_after();
-          const int halves = smin(2, chunks - 2 * pr);
-          for (int h = 0; h < halves; ++h) {
-            const uint32_t a_base = smem_u32(ring + st * kLaSlot + h * (kLaTile * 128));
-            const uint32_t b_base = smem_u32(smem + ly.q + (2 * pr + h) * NB * 128);
+          const uint64_t a = k_desc + (uint32_t)slot.st * (kLaSlot >> 4), b = q_desc + (uint32_t)k * (2 * NB * 128 >> 4);
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks)
+            umma_f16_if(leader, d, a + ks * 2, b + ks * 2, id_s, ks > 0 || k < pairs - 1);
+          if (2 * k + 1 < chunks)
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
-              umma_f16(d, sdesc_sw128(a_base + ks * 32, 16, 1024), sdesc_sw128(b_base + ks * 32, 16, 1024), id_s,
-                       (k | h | ks) ? 1u : 0u);
+              umma_f16_if(leader, d, a + (kLaTile * 128 >> 4) + ks * 2, b + (NB * 128 >> 4) + ks * 2, id_s, true);
+          if (k >= vblocks) {   // columns that are not values: done with
+            umma_commit_if(leader, &ctl->empty[slot.st]);
+            first = slot;
+            first.step(n_slots);
           }
-          if (pr >= vblocks) umma_commit(&ctl->empty[st]);   // columns that are not values: done with
         }
         if (!ok) break;
-        umma_commit(&ctl->s_full[n & 1]);
-        if (j == s.n - 1) umma_commit(&ctl->q_empty);
+        umma_commit_if(leader, &ctl->s_full[n & 1]);
+        if (j == s.n - 1) umma_commit_if(leader, &ctl->q_empty);
         if (due) ok = second();
         due = true;
         due_first = j == 0;
-        due_slot = my_slot;
+        due_slot = first;
         due_index = s.index;
         ++n;
       }
     }
     if (ok && due) second();
-  } else if (warp >= 2 && warp < 6) {
+  } else if (warp < 2 + kLaSoftmaxWarps) {
     // ------------------------------------------------------------- softmax
-    const int quad = warp & 3;
-    const int tid = threadIdx.x - 64;
+    // Two groups of four warps, each with half of the query rows and all tokens;
+    // nothing passes between them but their arrivals.
+    const int quad = warp & 3, grp = (warp - 2) >> 2, bar = 1 + grp, r0 = grp * (NB / 2);
+    const int tid = threadIdx.x - 64 - 128 * grp;
     const uint32_t lanes = (uint32_t)(quad * 32) << 16;
     const float to2 = p.scale * 1.4426950408889634f * (FP4 ? p.cache_scale : 1.0f);
     // requests without rows
-    for (int b = blockIdx.x; b < p.batch; b += gridDim.x)
+    for (int b = blockIdx.x; b < p.batch && grp == 0; b += gridDim.x)
       if (la_length(p, b) == 0) {
         for (int64_t i = tid; i < (int64_t)p.rows * p.rank; i += 128) p.out[(int64_t)b * p.rows * p.rank + i] = from_f<bf16>(0.0f);
         if (p.lse)
           for (int i = tid; i < p.rows; i += 128) p.lse[(int64_t)b * p.rows + i] = -CUDART_INF_F;
-        if (p.n_query > 1)
-          for (int i = tid; i < p.row_blocks; i += 128) p.flags[b * p.row_blocks + i] = 0;
+        for (int i = tid; i < p.row_blocks; i += 128) {
+          p.flags[b * p.row_blocks + i] = 0;
+          p.units[b * p.row_blocks + i] = make_int2(0, 1);
+        }
       }
     LaWalk walk(ctl);
     LaSegment s;
-    uint32_t n = 0, slot = 0;
+    uint32_t n = 0;
+    LaRing slot;
     bool ok = true;
-    constexpr int R = NB / 4;   // query rows a thread sees: 8 (i / 2) + 2 (lane % 4) + i % 2
+    constexpr int R = NB / 8;   // query rows a thread sees: r0 + 8 (i / 2) + 2 (lane % 4) + i % 2
     while (ok && walk.next(p, s)) {
       float m[R], l[R], mul[R];
 #pragma unroll
@@ -560,18 +626,18 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_co
       bool poison = false;
       for (int j = s.tile; j < s.tile + s.n; ++j, ++n) {
         const uint32_t buf = n & 1;
-        if (!mbar_wait(&ctl->s_full[buf], (n >> 1) & 1, p.status)) ctl->fail = 1;
+        if (!mbar_wait_within(&ctl->s_full[buf], (n >> 1) & 1, limit, p.status)) ctl->fail = 1;
         __syncwarp();
         tc_fence_after();
         uint32_t v[2 * R];
-        tmem_ld16x256<NB / 8>(tmem + lanes + kStatCols + buf * NB, v);
+        tmem_ld16x256<NB / 16>(tmem + lanes + kStatCols + buf * NB + r0, v);
         tmem_wait_ld();
         if constexpr (FP4) {
           if (j == s.tile) {
-            if (!mbar_wait(&ctl->q_full, (uint32_t)s.index & 1, p.status)) ctl->fail = 1;
+            if (!mbar_wait_within(&ctl->q_full, (uint32_t)s.index & 1, limit, p.status)) ctl->fail = 1;
 #pragma unroll
             for (int i = 0; i < R; ++i)
-              mul[i] = to2 * exp2f((float)-ctl->qexp[s.index & 1][8 * (i >> 1) + 2 * (lane & 3) + (i & 1)]);
+              mul[i] = to2 * exp2f((float)-ctl->qexp[s.index & 1][r0 + 8 * (i >> 1) + 2 * (lane & 3) + (i & 1)]);
           }
         }
         const int tok = j * kLaTile + quad * 16 + (lane >> 2);
@@ -582,15 +648,19 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_co
         for (int i = 0; i < R; ++i) {
           y0[i] = __uint_as_float(v[4 * (i >> 1) + (i & 1)]) * mul[i];
           y1[i] = __uint_as_float(v[4 * (i >> 1) + 2 + (i & 1)]) * mul[i];
-          if (edge) {
-            const int row = s.rb * NB + 8 * (i >> 1) + 2 * (lane & 3) + (i & 1);
-            const int sees = p.n_query == 1 ? all_see : all_see + smin(row, p.rows - 1) / p.n_heads;
+        }
+        if (edge) {
+#pragma unroll
+          for (int i = 0; i < R; ++i) {
+            int sees = all_see;
+            if (p.n_query > 1) sees += smin(s.rb * NB + r0 + 8 * (i >> 1) + 2 * (lane & 3) + (i & 1), p.rows - 1) / p.n_heads;
             if (tok >= sees) y0[i] = -CUDART_INF_F;
             if (tok + 8 >= sees) y1[i] = -CUDART_INF_F;
           }
-          over |= fmaxf(y0[i], y1[i]) > m[i] + kLaLift;
         }
-        over = la_bar_any(over);
+#pragma unroll
+        for (int i = 0; i < R; ++i) over |= fmaxf(y0[i], y1[i]) > m[i] + kLaLift;
+        over = la_bar_any(bar, over);
         if (ctl->fail) {
           ok = false;
           break;
@@ -601,22 +671,28 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_co
           // not must be finite, or the unit is computed again by the combine
           // kernel.
           const int valid = smin(s.len - j * kLaTile, kLaTile), shared_rows = smax(all_see - j * kLaTile, 0);
-          for (int k = pairs - vblocks; k < pairs; ++k) {
-            const uint32_t sl = slot + k;
-            if (!mbar_wait(&ctl->full[sl % n_slots], (sl / n_slots) & 1, p.status)) ctl->fail = 1;
-            unsigned char *base = ring + (sl % n_slots) * kLaSlot;
+          LaRing at = slot;
+          for (int k = 0; k < pairs; ++k, at.step(n_slots)) {
+            if (k < pairs - vblocks) continue;
+            if (!mbar_wait_within(&ctl->full[at.st], at.turn & 1, limit, p.status)) ctl->fail = 1;
+            unsigned char *base = ring + at.st * kLaSlot;
             const int halves = smin(2, chunks - 2 * (pairs - 1 - k));
             for (int h = 0; h < halves; ++h) {
               unsigned char *half = base + h * (kLaTile * 128);
-              for (int i = valid * 8 + tid; i < kLaTile * 8; i += 128)
-                *reinterpret_cast<uint4 *>(half + i * 16) = make_uint4(0u, 0u, 0u, 0u);
-              if (p.n_query > 1)
+              if (h == grp || halves == 1)   // a single half by both
+                for (int i = valid * 8 + tid; i < kLaTile * 8; i += 128)
+                  *reinterpret_cast<uint4 *>(half + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+              if (p.n_query > 1 && grp == 0)
                 for (int i = shared_rows * 8 + tid; i < valid * 8; i += 128)
                   poison |= la_not_finite<FP4>(*reinterpret_cast<const uint4 *>(half + i * 16));
             }
           }
         }
-        slot += pairs;
+        slot.st += pairs;   // pairs <= n_slots
+        if (slot.st >= n_slots) {
+          slot.st -= n_slots;
+          ++slot.turn;
+        }
         if (over) {
           // New reference: the largest logit of each query row so far.
 #pragma unroll
@@ -624,12 +700,12 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_co
             float t = fmaxf(y0[i], y1[i]);
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
-            if (lane < 4) ctl->wmax[quad][8 * (i >> 1) + 2 * lane + (i & 1)] = t;
+            if (lane < 4) ctl->wmax[quad][r0 + 8 * (i >> 1) + 2 * lane + (i & 1)] = t;
           }
-          la_bar();
+          la_bar(bar);
 #pragma unroll
           for (int i = 0; i < R; ++i) {
-            const int row = 8 * (i >> 1) + 2 * (lane & 3) + (i & 1);
+            const int row = r0 + 8 * (i >> 1) + 2 * (lane & 3) + (i & 1);
             float t = m[i];
 #pragma unroll
             for (int w = 0; w < 4; ++w) t = fmaxf(t, ctl->wmax[w][row]);
@@ -638,26 +714,31 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_co
             l[i] *= f;
             if (quad == 0 && lane < 4) ctl->fac[row] = f;
           }
-          la_bar();
+          la_bar(bar);
           if (j > s.tile) {
-            if (!mbar_wait(&ctl->pv_done[(n - 1) & 1], ((n - 1) >> 1) & 1, p.status)) ctl->fail = 1;
+            if (!mbar_wait_within(&ctl->pv_done, (n - 1) & 1, limit, p.status)) ctl->fail = 1;
             __syncwarp();
             tc_fence_after();
-            for (int c = 0; c < vblocks * NB; c += 16) {
-              uint32_t w[16];
-              tmem_ld16(tmem + lanes + c, w);
-              tmem_wait_ld();
+            for (int c = r0; c < r0 + NB / 2; c += 8) {
+              float f[8];
 #pragma unroll
-              for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * ctl->fac[(c + i) % NB]);
-              tmem_st16(tmem + lanes + c, w);
+              for (int i = 0; i < 8; ++i) f[i] = ctl->fac[c + i];
+              for (int vb = 0; vb < vblocks; ++vb) {
+                uint32_t w[8];
+                tmem_ld8(tmem + lanes + vb * NB + c, w);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * f[i]);
+                tmem_st8(tmem + lanes + vb * NB + c, w);
+              }
             }
             tmem_wait_st();
           }
         }
         // P^T: token lines of NB query rows, swizzled; free once the products
-        // of tile n - 2 are done.
-        if (n >= 2 && !mbar_wait(&ctl->pv_done[buf], ((n - 2) >> 1) & 1, p.status)) ctl->fail = 1;
-        unsigned char *pb = smem + ly.p + buf * (kLaTile * 128);
+        // of tile n - 1 are done.
+        if (n >= 1 && !mbar_wait_within(&ctl->pv_done, (n - 1) & 1, limit, p.status)) ctl->fail = 1;
+        unsigned char *pb = smem + ly.p;
         const int t0 = quad * 16 + (lane >> 2);
 #pragma unroll
         for (int i = 0; i < R; i += 2) {
@@ -666,33 +747,33 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_co
           const float p10 = ex2_approx(y1[i] - a), p11 = ex2_approx(y1[i + 1] - b);
           l[i] += p00 + p10;
           l[i + 1] += p01 + p11;
-          const uint32_t at = (uint32_t)((((i >> 1) ^ (t0 & 7)) << 4) + (lane & 3) * 4);
+          const uint32_t at = (uint32_t)((((r0 / 8 + (i >> 1)) ^ (t0 & 7)) << 4) + (lane & 3) * 4);
           *reinterpret_cast<uint32_t *>(pb + t0 * 128 + at) = FP4 ? pack_half(p00, p01) : pack_bf16(p00, p01);
           *reinterpret_cast<uint32_t *>(pb + (t0 + 8) * 128 + at) = FP4 ? pack_half(p10, p11) : pack_bf16(p10, p11);
         }
         fence_async_smem();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl->p_full[buf]);
+        if (lane == 0) mbar_arrive(&ctl->p_full);
       }
       if (!ok) break;
       // End of the segment: sums over the tokens, then the result.
-      la_bar();   // wmax is free
+      la_bar(bar);   // wmax is free
 #pragma unroll
       for (int i = 0; i < R; ++i) {
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], o);
-        if (lane < 4) ctl->wmax[quad][8 * (i >> 1) + 2 * lane + (i & 1)] = l[i];
+        if (lane < 4) ctl->wmax[quad][r0 + 8 * (i >> 1) + 2 * lane + (i & 1)] = l[i];
       }
       const bool whole = s.n == s.unit_tiles;
       const int part = 2 * (int)blockIdx.x + (s.index > 0 ? 1 : 0);
       const int rows = smin(NB, p.rows - s.rb * NB);
       const int64_t row0 = (int64_t)s.b * p.rows + s.rb * NB;
-      la_bar();
+      la_bar(bar);
       if (quad == 0 && lane < 4) {
 #pragma unroll
         for (int i = 0; i < R; ++i) {
-          const int row = 8 * (i >> 1) + 2 * lane + (i & 1);
+          const int row = r0 + 8 * (i >> 1) + 2 * lane + (i & 1);
           const float sum = (ctl->wmax[0][row] + ctl->wmax[1][row]) + (ctl->wmax[2][row] + ctl->wmax[3][row]);
           if (whole) {
             ctl->fac[row] = sum > 0.0f || sum != sum ? (FP4 ? p.cache_scale : 1.0f) / sum : 0.0f;
@@ -703,35 +784,42 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_co
           }
         }
       }
-      if (p.n_query > 1 && s.tile + s.n == s.unit_tiles) {
-        const bool any = la_bar_any(poison);
-        if (tid == 0) p.flags[s.b * p.row_blocks + s.rb] = any ? 1 : 0;
-      } else {
-        la_bar();
+      // The CTA with a unit's first tile says which parts there will be: its
+      // own one (the second if it began with another unit) and the first one
+      // of each CTA behind it.
+      if (s.tile == 0 && tid == 0 && grp == 0) {
+        const int rest = s.unit_tiles - s.n, share = ctl->share;
+        p.units[s.b * p.row_blocks + s.rb] = make_int2(part, 1 + (rest + share - 1) / share);
       }
-      if (!mbar_wait(&ctl->pv_done[(n - 1) & 1], ((n - 1) >> 1) & 1, p.status)) ctl->fail = 1;
+      if (p.n_query > 1 && s.tile + s.n == s.unit_tiles) {
+        const bool any = la_bar_any(bar, poison);
+        if (tid == 0 && grp == 0) p.flags[s.b * p.row_blocks + s.rb] = any ? 1 : 0;
+      } else {
+        la_bar(bar);
+      }
+      if (!mbar_wait_within(&ctl->pv_done, (n - 1) & 1, limit, p.status)) ctl->fail = 1;
       __syncwarp();
       tc_fence_after();
       for (int vb = 0; vb < vblocks; ++vb) {
         const int col = vb * 128 + quad * 32 + lane;
-        for (int c = 0; c < NB; c += 16) {
-          uint32_t w[16];
+        bf16 *out = p.out + (row0 + r0) * p.rank + col;
+        float *pt = p.part + ((int64_t)part * NB + r0) * p.rank + col;
+        for (int c = r0; c < r0 + NB / 2 && c < rows; c += 8) {
+          uint32_t w[8];
           __syncwarp();
-          tmem_ld16(tmem + lanes + vb * NB + c, w);
+          tmem_ld8(tmem + lanes + vb * NB + c, w);
           tmem_wait_ld();
-          if (col < p.rank) {
+          const int live = col < p.rank ? rows - c : 0;
+          if (whole) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const int row = c + i;
-              if (row < rows) {
-                if (whole) {
-                  const float f = ctl->fac[row];
-                  p.out[(row0 + row) * p.rank + col] = from_f<bf16>(f == 0.0f ? 0.0f : __uint_as_float(w[i]) * f);
-                } else {
-                  p.part[((int64_t)part * NB + row) * p.rank + col] = __uint_as_float(w[i]);
-                }
-              }
+            for (int i = 0; i < 8; ++i, out += p.rank) {
+              const float f = ctl->fac[c + i];
+              if (i < live) *out = from_f<bf16>(f == 0.0f ? 0.0f : __uint_as_float(w[i]) * f);
             }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i, pt += p.rank)
+              if (i < live) *pt = __uint_as_float(w[i]);
           }
         }
       }
@@ -739,16 +827,18 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_co
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl->o_free);
     }
-  } else if (FP4 && warp >= 6) {
+  } else if (FP4) {
     // -------------------------------------------------------- 4-bit to fp16
-    const int tid = threadIdx.x - 192, dw = warp - 6;
+    const int dw = warp - 2 - kLaSoftmaxWarps, my = dw / kLaDequantGroup;
     LaWalk walk(ctl);
     LaSegment s;
-    uint32_t slot = 0, raw = 0;
+    constexpr int kGroups = kLaDequantWarps / kLaDequantGroup;
+    LaRing slot, raw;
+    int turn = 0;   // the group whose slot is next
     bool ok = true;
     while (ok && walk.next(p, s)) {
       // queries: one warp a row, scaled so that the largest value lies in [2^14, 2^15)
-      if (s.index > 0 && !mbar_wait(&ctl->q_empty, (uint32_t)(s.index - 1) & 1, p.status)) break;
+      if (s.index > 0 && !mbar_wait_within(&ctl->q_empty, (uint32_t)(s.index - 1) & 1, limit, p.status)) break;
       for (int row = dw; row < NB; row += kLaDequantWarps) {
         const bool live = s.rb * NB + row < p.rows;
         const bf16 *src = p.q + ((int64_t)s.b * p.rows + s.rb * NB + row) * p.width;
@@ -767,7 +857,7 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_co
         }
         top = warp_max(top);
         const int e = top > 0.0f && top < CUDART_INF_F ? 14 - ilogbf(top) : 0;
-        if (lane == 0) ctl->qexp[s.index & 1][row] = e;
+        if (lane == 0) ctl->qexp[s.index & 1][row] = (int16_t)e;
         const float f = ldexpf(1.0f, e / 2), g = ldexpf(1.0f, e - e / 2);   // 2^e may leave fp32's range
 #pragma unroll
         for (int c = 0; c < (S4R_MAX_LATENT_WIDTH + 63) / 64; ++c)
@@ -778,38 +868,45 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_co
       fence_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl->q_full);
-      const int tok = tid & 63, quarter = tid >> 6;
-      for (int j = 0; j < s.n && ok; ++j, ++raw) {
-        const int st = (int)(raw % kLaRawStages);
-        ok = mbar_wait(&ctl->raw_full[st], (raw / kLaRawStages) & 1, p.status);
+      // Ring slots: a group of two warps takes every fourth, a thread one token
+      // of it, 128 columns.
+      const int tok = (dw % kLaDequantGroup) * 32 + lane;
+      for (int j = 0; j < s.n && ok; ++j, raw.step(kLaRawStages)) {
+        const int st = raw.st;
+        ok = mbar_wait_within(&ctl->raw_full[st], raw.turn & 1, limit, p.status);
         const unsigned char *src = smem + ly.raw + st * la_raw_bytes(p.width);
-        for (int k = 0; k < pairs && ok; ++k, ++slot) {
-          const int pr = pairs - 1 - k, sl = (int)(slot % n_slots);
-          if (slot >= (uint32_t)n_slots) ok = mbar_wait(&ctl->empty[sl], ((slot / n_slots) - 1) & 1, p.status);
-          if (!ok) break;
-          const int col = pr * 128 + quarter * 32;
-          unsigned char *line = ring + sl * kLaSlot + (quarter >> 1) * (kLaTile * 128) + tok * 128;
-          uint4 code = make_uint4(0u, 0u, 0u, 0u);
-          __half2 sc[2] = {__half2half2(__ushort_as_half(0)), __half2half2(__ushort_as_half(0))};
-          if (col < p.width) {
-            code = *reinterpret_cast<const uint4 *>(src + tok * (p.width / 2) + col / 2);
-            const unsigned short two =
-                *reinterpret_cast<const unsigned short *>(src + kLaTile * (p.width / 2) + tok * (p.width / 16) + col / 16);
-            const __half2 both = __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3));
-            sc[0] = __half2half2(__low2half(both));
-            sc[1] = __half2half2(__high2half(both));
+        for (int pr = pairs - 1; pr >= 0 && ok; --pr, slot.step(n_slots), turn = (turn + 1) % kGroups) {
+          if (turn != my) continue;
+          const int sl = slot.st;
+          const unsigned char *codes = src + tok * (p.width / 2) + pr * 64;
+          const unsigned char *scales = src + kLaTile * (p.width / 2) + tok * (p.width / 16) + pr * 8;
+          uint4 code[4];
+          unsigned short two[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const bool in = pr * 128 + c * 32 < p.width;   // columns behind the row are zeros
+            code[c] = in ? *reinterpret_cast<const uint4 *>(codes + c * 16) : make_uint4(0u, 0u, 0u, 0u);
+            two[c] = in ? *reinterpret_cast<const unsigned short *>(scales + c * 2) : (unsigned short)0;
           }
-          const uint32_t w[4] = {code.x, code.y, code.z, code.w};
+          if (slot.turn > 0) ok = mbar_wait_within(&ctl->empty[sl], (slot.turn - 1) & 1, limit, p.status);
+          if (!ok) break;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t o[4];
+          for (int c = 0; c < 4; ++c) {
+            unsigned char *line = ring + sl * kLaSlot + (c >> 1) * (kLaTile * 128) + tok * 128;
+            const __half2 both = __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two[c], __NV_E4M3));
+            const __half2 sc[2] = {__half2half2(__low2half(both)), __half2half2(__high2half(both))};
+            const uint32_t w[4] = {code[c].x, code[c].y, code[c].z, code[c].w};
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
-              const __half2 h = __hmul2(
-                  __half2(__nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)(w[i] >> (8 * b)), __NV_E2M1)), sc[i >> 1]);
-              o[b] = (uint32_t)__half_as_ushort(__low2half(h)) | ((uint32_t)__half_as_ushort(__high2half(h)) << 16);
+            for (int i = 0; i < 4; ++i) {
+              uint32_t o[4];
+#pragma unroll
+              for (int b = 0; b < 4; ++b) {
+                const __half2 h = __hmul2(
+                    __half2(__nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)(w[i] >> (8 * b)), __NV_E2M1)), sc[i >> 1]);
+                o[b] = (uint32_t)__half_as_ushort(__low2half(h)) | ((uint32_t)__half_as_ushort(__high2half(h)) << 16);
+              }
+              *reinterpret_cast<uint4 *>(line + ((((c & 1) * 4 + i) ^ (tok & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
             }
-            *reinterpret_cast<uint4 *>(line + ((((quarter & 1) * 4 + i) ^ (tok & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
           }
           fence_async_smem();
           __syncwarp();
@@ -839,7 +936,8 @@ __device__ __forceinline__ float latent_value(const LatentAttend &p, int64_t pag
   }
 }
 
-// Joins the partial sums of one query row, 128 columns a CTA:
+// Joins the partial sums of one query row (and of `cols` columns, a multiple
+// of 128 that is less than the rank when there are few rows), a CTA each:
 //   out = sum_k 2^(m_k - m) O_k / sum_k 2^(m_k - m) l_k, m = max_k m_k.
 // Units that one CTA computed whole are skipped.  A unit whose flag is set
 // (rows that only some of its query rows see hold infinities or NaN, which a
@@ -847,20 +945,22 @@ __device__ __forceinline__ float latent_value(const LatentAttend &p, int64_t pag
 // computed again here, row by row over the rows it sees: rare, and slow.
 constexpr int kLcThreads = 128;
 template <int NB, bool FP4>
-__global__ void __launch_bounds__(kLcThreads) latent_combine_kernel(const LatentAttend p) {
-  __shared__ long long scratch[2 * kLcThreads / 32];
-  __shared__ float sm[kLcThreads / 32], sl[kLcThreads / 32], sacc[kLcThreads / 32][kLcThreads];
+__global__ void __launch_bounds__(kLcThreads) latent_combine_kernel(const LatentAttend p, const int cols) {
+  __shared__ __align__(16) float sm[kLcThreads / 32], sl[kLcThreads / 32], sacc[kLcThreads / 32][S4R_MAX_LATENT_RANK], f_s[kLcThreads];
   const int row = blockIdx.x % p.rows, b = blockIdx.x / p.rows, rb = row / NB;
-  const int col = blockIdx.y * 128 + threadIdx.x;
   const int64_t at = (int64_t)b * p.rows + row;
   pdl_wait();
-  const int len = la_length(p, b), nt = la_tiles(len);
-  if (nt == 0) return;
-  if (p.n_query > 1 && p.flags[b * p.row_blocks + rb]) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int sees = len - p.n_query + 1 + row / p.n_heads;
-    float m = -CUDART_INF_F, l = 0.0f, acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int i = warp; i < sees; i += kLcThreads / 32) {
+  const int unit = b * p.row_blocks + rb;
+  const int2 parts = p.units[unit];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  constexpr int W = kLcThreads / 32, kCols = S4R_MAX_LATENT_RANK / 32;
+  if (p.n_query > 1 && p.flags[unit]) {
+    if (blockIdx.y > 0) return;
+    const int sees = la_length(p, b) - p.n_query + 1 + row / p.n_heads;
+    float m = -CUDART_INF_F, l = 0.0f, acc[kCols];
+#pragma unroll
+    for (int k = 0; k < kCols; ++k) acc[k] = 0.0f;
+    for (int i = warp; i < sees; i += W) {
       const int32_t page = p.block_table[(int64_t)b * p.max_pages + (i >> p.page_shift)];
       if (page < 0 || page >= p.n_pages) continue;   // reported by the main kernel
       const int32_t r = i & (p.page_size - 1);
@@ -872,8 +972,8 @@ __global__ void __launch_bounds__(kLcThreads) latent_combine_kernel(const Latent
       l = l * f + e;
       m = top;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int c = blockIdx.y * 128 + k * 32 + lane;
+      for (int k = 0; k < kCols; ++k) {
+        const int c = k * 32 + lane;
         if (c < p.rank) acc[k] = acc[k] * f + e * latent_value<FP4>(p, page, r, c);
       }
     }
@@ -882,42 +982,90 @@ __global__ void __launch_bounds__(kLcThreads) latent_combine_kernel(const Latent
       sl[warp] = l;
     }
 #pragma unroll
-    for (int k = 0; k < 4; ++k) sacc[warp][k * 32 + lane] = acc[k];
+    for (int k = 0; k < kCols; ++k) sacc[warp][k * 32 + lane] = acc[k];
     __syncthreads();
-    float top = -CUDART_INF_F, sum = 0.0f, o = 0.0f;
-    for (int w = 0; w < kLcThreads / 32; ++w) top = fmaxf(top, sm[w]);
-    for (int w = 0; w < kLcThreads / 32; ++w) {
-      const float f = sl[w] == 0.0f ? 0.0f : expf(sm[w] - top);
-      if (sl[w] != 0.0f) {
-        sum += f * sl[w];
-        o += f * sacc[w][threadIdx.x];
-      }
+    float top = -CUDART_INF_F, sum = 0.0f;
+    for (int w = 0; w < W; ++w) top = fmaxf(top, sm[w]);
+    for (int w = 0; w < W; ++w) sum += sl[w] == 0.0f ? 0.0f : expf(sm[w] - top) * sl[w];
+    for (int c = threadIdx.x; c < p.rank; c += kLcThreads) {
+      float o = 0.0f;
+      for (int w = 0; w < W; ++w) o += sl[w] == 0.0f ? 0.0f : expf(sm[w] - top) * sacc[w][c];
+      p.out[at * p.rank + c] = from_f<bf16>(sees > 0 ? o / sum : 0.0f);
     }
-    if (col < p.rank) p.out[at * p.rank + col] = from_f<bf16>(sees > 0 ? o / sum : 0.0f);
-    if (p.lse && blockIdx.y == 0 && threadIdx.x == 0) p.lse[at] = sees > 0 ? top + logf(sum) : -CUDART_INF_F;
+    if (p.lse && threadIdx.x == 0) p.lse[at] = sees > 0 ? top + logf(sum) : -CUDART_INF_F;
     return;
   }
-  long long total, before;
-  la_count(p, b, scratch, total, before);
-  const long long share = la_share(total, p.n_ctas);
-  const long long first = before + (long long)rb * nt, last = first + nt - 1;
-  const int c0 = (int)(first / share), c1 = (int)(last / share);
-  if (c0 == c1) return;
+  if (parts.y <= 1) return;
+  // Part 0 lies in slot parts.x, the others in the first slot of the CTAs
+  // behind it.  Statistics first, a thread a part; then the warps share out the
+  // parts, a lane adding up 4 neighbouring columns of every 128.
   const int r = row - rb * NB;
+  auto slot_of = [&](int i) { return (int64_t)(i == 0 ? parts.x : 2 * (parts.x / 2 + i)) * NB + r; };
   float top = -CUDART_INF_F;
-  for (int c = c0; c <= c1; ++c) top = fmaxf(top, p.ml[(int64_t)(2 * c + (first > c * share ? 1 : 0)) * NB + r].x);
-  float sum = 0.0f, o = 0.0f;
-  for (int c = c0; c <= c1; ++c) {
-    const int64_t k = (int64_t)(2 * c + (first > c * share ? 1 : 0)) * NB + r;
-    const float2 ml = p.ml[k];
-    if (ml.x == -CUDART_INF_F && ml.y == 0.0f) continue;   // this part saw nothing
-    const float f = exp2f(ml.x - top);
-    sum = fmaf(f, ml.y, sum);
-    if (col < p.rank) o = fmaf(f, p.part[k * p.rank + col], o);
+  for (int i = threadIdx.x; i < parts.y; i += kLcThreads) top = fmaxf(top, p.ml[slot_of(i)].x);
+  top = warp_max(top);
+  if (lane == 0) sm[warp] = top;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < W; ++w) top = fmaxf(top, sm[w]);
+  float sum = 0.0f;
+  float4 o[S4R_MAX_LATENT_RANK / 128];
+#pragma unroll
+  for (int k = 0; k < S4R_MAX_LATENT_RANK / 128; ++k) o[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  const int col0 = blockIdx.y * cols + 4 * lane, col1 = smin((int)(blockIdx.y + 1) * cols, p.rank);
+  for (int base = 0; base < parts.y; base += kLcThreads) {
+    const int m = smin(parts.y - base, kLcThreads);
+    float f = 0.0f, part_sum = 0.0f;
+    if ((int)threadIdx.x < m) {
+      const float2 ml = p.ml[slot_of(base + threadIdx.x)];
+      // a part that saw nothing has no reference
+      f = ml.x == -CUDART_INF_F && ml.y == 0.0f ? 0.0f : exp2f(ml.x - top);
+      part_sum = f == 0.0f ? 0.0f : f * ml.y;
+    }
+    part_sum = warp_sum(part_sum);
+    __syncthreads();
+    f_s[threadIdx.x] = f;
+    if (lane == 0) sl[warp] = part_sum;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < W; ++w) sum += sl[w];
+#pragma unroll 4
+    for (int i = warp; i < m; i += W) {
+      const float w = f_s[i];
+      const float *src = p.part + slot_of(base + i) * p.rank;
+#pragma unroll
+      for (int k = 0; k < S4R_MAX_LATENT_RANK / 128; ++k) {
+        const int col = col0 + 128 * k;
+        if (col < col1 && w != 0.0f) {   // a part of weight 0 may hold infinities
+          const float4 x = *reinterpret_cast<const float4 *>(src + col);
+          o[k].x = fmaf(w, x.x, o[k].x);
+          o[k].y = fmaf(w, x.y, o[k].y);
+          o[k].z = fmaf(w, x.z, o[k].z);
+          o[k].w = fmaf(w, x.w, o[k].w);
+        }
+      }
+    }
   }
+#pragma unroll
+  for (int k = 0; k < S4R_MAX_LATENT_RANK / 128; ++k)
+    *reinterpret_cast<float4 *>(&sacc[warp][128 * k + 4 * lane]) = o[k];
+  __syncthreads();
   const bool none = top == -CUDART_INF_F && sum == 0.0f;
-  if (col < p.rank) p.out[at * p.rank + col] = from_f<bf16>(none ? 0.0f : o * (p.cache_scale / sum));
-  if (p.lse && blockIdx.y == 0 && threadIdx.x == 0)
+  const float f = none ? 0.0f : p.cache_scale / sum;
+  const int at_col = 4 * threadIdx.x, col = blockIdx.y * cols + at_col;
+  if (col < col1) {
+    float4 t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (!none)
+      for (int w = 0; w < W; ++w) {
+        const float4 x = *reinterpret_cast<const float4 *>(&sacc[w][at_col]);
+        t.x += x.x;
+        t.y += x.y;
+        t.z += x.z;
+        t.w += x.w;
+      }
+    *reinterpret_cast<uint2 *>(p.out + at * p.rank + col) = make_uint2(pack_bf16(t.x * f, t.y * f), pack_bf16(t.z * f, t.w * f));
+  }
+  if (p.lse && threadIdx.x == 0 && blockIdx.y == 0)
     p.lse[at] = none ? -CUDART_INF_F : (top + log2f(sum)) * 0.6931471805599453f;
 }
 
