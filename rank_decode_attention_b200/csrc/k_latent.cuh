@@ -297,6 +297,18 @@ __device__ __forceinline__ void bulk_load_if(uint32_t on, void *dst, const void 
       "l"(src), "r"(bytes), "r"(smem_u32(bar)), "r"(on)
       : "memory");
 }
+// Whether the phase of the given parity has completed, without waiting.
+__device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 // kind::f16 with fp16 operands instead of bf16 ones.
 __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, int a_mn_major, int b_mn_major) {
   return idesc_bf16_f32(M, N, a_mn_major, b_mn_major) & ~((7u << 7) | (7u << 10));
@@ -525,6 +537,7 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_co
     const uint64_t v_desc = sdesc_sw128(smem_u32(ring), kLaTile * 128, 1024);
     const uint64_t p_desc = sdesc_sw128(smem_u32(smem + ly.p), kLaTile * 128, 1024);
     auto wait = [&](uint64_t *bar, uint32_t parity) { return __shfl_sync(0xffffffffu, (int)mbar_wait_within(bar, parity & 1, limit, p.status), 0) != 0; };
+    auto ready = [&](uint64_t *bar, uint32_t parity) { return __shfl_sync(0xffffffffu, (int)mbar_test(bar, parity & 1), 0) != 0; };
     LaRing slot;
     uint32_t n = 0;                      // tiles so far
     bool due = false, due_first = false; // the tile before waits for its second product; it is its unit's first
@@ -535,7 +548,7 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_co
       if (due_first && due_index > 0 && !wait(&ctl->o_free, (uint32_t)(due_index - 1))) return false;
       tc_fence_after();
       for (int vb = vblocks - 1; vb >= 0; --vb, due_slot.step(n_slots)) {
-        const uint64_t a = v_desc + (uint32_t)due_slot.st * (kLaSlot >> 4);
+        const uint64_t a = v_desc + (uint32_t)__shfl_sync(0xffffffffu, due_slot.st, 0) * (kLaSlot >> 4);
 #pragma unroll
         for (int ks = 0; ks < kLaTile / 16; ++ks)
           umma_f16_if(leader, tmem + vb * NB, a + ks * (2048 >> 4), p_desc + ks * (2048 >> 4), id_o, ks > 0 || !due_first);
@@ -555,18 +568,21 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_co
         const uint32_t d = tmem + kStatCols + (n & 1) * NB;
         LaRing first = slot;
         for (int k = pairs - 1; k >= 0 && ok; --k, slot.step(n_slots)) {
-          // a slot that the tile before still holds comes free with its second product
-          if (due && slot.turn > 0 && (slot.turn - 1 > due_slot.turn || (slot.turn - 1 == due_slot.turn && slot.st >= due_slot.st))) {
+          // The second product of the tile before goes first once its
+          // probabilities are there (its slots are then free early), or if
+          // this slot comes free only with it.
+          if (due && (ready(&ctl->p_full, n - 1) ||
+                      (slot.turn > 0 && (slot.turn - 1 > due_slot.turn || (slot.turn - 1 == due_slot.turn && slot.st >= due_slot.st))))) {
             ok = second();
             due = false;
           }
           if (ok) ok = wait(&ctl->full[slot.st], slot.turn);
           if (!ok) break;
           tc_fence_after();
-          const uint64_t a = k_desc + (uint32_t)slot.st * (kLaSlot >> 4), b = q_desc + (uint32_t)k * (2 * NB * 128 >> 4);
+          const uint64_t a = k_desc + (uint32_t)__shfl_sync(0xffffffffu, slot.st, 0) * (kLaSlot >> 4), b = q_desc + (uint32_t)k * (2 * NB * 128 >> 4);
+          umma_f16_if(leader, d, a, b, id_s, k < pairs - 1);
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
-            umma_f16_if(leader, d, a + ks * 2, b + ks * 2, id_s, ks > 0 || k < pairs - 1);
+          for (int ks = 1; ks < 4; ++ks) umma_f16_if(leader, d, a + ks * 2, b + ks * 2, id_s, true);
           if (2 * k + 1 < chunks)
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
