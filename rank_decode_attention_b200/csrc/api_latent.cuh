@@ -122,6 +122,34 @@ s4r_status latent_attend_launch(const LatentAttend &p, cudaStream_t st) {
   return err == cudaSuccess ? S4R_OK : fail("latent_combine_kernel", err);
 }
 
+// Column tiles of a projection with NT columns a tile, and what the longest
+// CTA then computes.
+struct LpTiles {
+  int32_t n_tiles;
+  int64_t cost;
+};
+template <int NT>
+LpTiles lp_tiles(const LatentProject &p) {
+  constexpr int kGroups = NT / 64;
+  LpTiles t;
+  t.n_tiles = (int32_t)(p.shared_x ? ceil_div((int64_t)p.n_heads * p.head_groups, kGroups)
+                                   : p.n_heads * ceil_div(p.head_groups, kGroups));
+  const int widest = smin(kGroups, p.shared_x ? p.n_heads * p.head_groups : p.head_groups);
+  t.cost = ceil_div((int64_t)t.n_tiles * p.m_tiles, sm_count()) * widest;
+  return t;
+}
+
+template <int NT>
+s4r_status latent_project_launch(const CUtensorMap &mx, const CUtensorMap &mb, const CUtensorMap &mo, LatentProject p,
+                                 int32_t n_tiles, cudaStream_t st) {
+  p.n_tiles = n_tiles;
+  const cudaError_t err = ensure_smem<latent_project_kernel<NT>>(kLpSmem);
+  if (err != cudaSuccess) return fail("latent_project_kernel (shared memory)", err);
+  const unsigned grid = grid_of((int64_t)n_tiles * p.m_tiles, sm_count());
+  latent_project_kernel<NT><<<grid, kLpThreads, kLpSmem, st>>>(mx, mb, mo, p);
+  return check_launch("latent_project_kernel");
+}
+
 }  // namespace
 
 extern "C" {
@@ -256,11 +284,40 @@ s4r_status s4r_latent_project(const s4r_latent_project_args *a, void *stream) {
   if (a->x_ts < 0 || a->x_hs < 0 || a->out_ts < 0 || a->out_hs < 0) return S4R_ERR_INVALID_ARG;
   if ((a->n_tokens > 1 && a->x_ts < n_in) || (a->x_hs != 0 && a->x_hs < n_in) || !apart(a->out_ts, a->out_hs, n_out))
     return S4R_ERR_INVALID_ARG;
-  LatentProject p{a->n_tokens, a->n_heads, a->head_dim, a->rank, a->to_latent, static_cast<const bf16 *>(a->x),
-                  static_cast<const bf16 *>(a->basis), static_cast<bf16 *>(a->out), a->x_ts, a->x_hs, a->out_ts, a->out_hs};
+  const bool shared = a->x_hs == 0 && a->n_heads > 1;
+  LatentProject p{};
+  p.n_tokens = (int32_t)a->n_tokens;
+  p.n_heads = a->n_heads;
+  p.n_in = (int32_t)n_in;
+  p.to_latent = a->to_latent ? 1 : 0;
+  p.shared_x = shared ? 1 : 0;
+  p.head_groups = (int32_t)ceil_div(n_out, 64);
+  p.m_tiles = (int32_t)ceil_div(a->n_tokens, 128);
+  // A dimension of one row needs no stride of the caller's.
+  const uint64_t xs[2] = {shared || a->n_heads == 1 ? (uint64_t)n_in * 2 : (uint64_t)a->x_hs * 2,
+                          a->n_tokens == 1 ? (uint64_t)n_in * 2 : (uint64_t)a->x_ts * 2};
+  const uint64_t xd[3] = {(uint64_t)n_in, shared ? 1u : (uint64_t)a->n_heads, (uint64_t)a->n_tokens};
+  const uint32_t xb[3] = {64, 1, 128};
+  const uint64_t bs[2] = {(uint64_t)a->rank * 2, (uint64_t)a->rank * a->head_dim * 2};
+  const uint64_t bd[3] = {(uint64_t)a->rank, (uint64_t)a->head_dim, (uint64_t)a->n_heads};
+  const uint32_t bb[3] = {64, 64, 1};
+  const uint64_t os[2] = {a->n_heads == 1 ? (uint64_t)n_out * 2 : (uint64_t)a->out_hs * 2,
+                          a->n_tokens == 1 ? (uint64_t)n_out * 2 : (uint64_t)a->out_ts * 2};
+  const uint64_t od[3] = {(uint64_t)n_out, (uint64_t)a->n_heads, (uint64_t)a->n_tokens};
+  const uint32_t ob[3] = {64, 1, 32};
+  CUtensorMap mx, mb, mo;
+  if (!make_tmap_bf16_nd(&mx, a->x, 3, xd, xs, xb) || !make_tmap_bf16_nd(&mb, a->basis, 3, bd, bs, bb) ||
+      !make_tmap_bf16_nd(&mo, a->out, 3, od, os, ob)) {
+    snprintf(g_last_error, sizeof(g_last_error), "cuTensorMapEncodeTiled failed for s4r_latent_project");
+    return S4R_ERR_CUDA;
+  }
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  latent_project_simt<<<grid_of(ceil_div(a->n_tokens * a->n_heads * n_out, 256), 64 * sm_count()), 256, 0, st>>>(p);
-  return check_launch("latent_project");
+  const LpTiles t256 = lp_tiles<256>(p), t128 = lp_tiles<128>(p), t64 = lp_tiles<64>(p);
+  // The widest tile unless a narrower one ends earlier (rounds of the grid x
+  // columns): a call with few tokens has only its heads' columns to spread.
+  if (t256.cost <= t128.cost && t256.cost <= t64.cost) return latent_project_launch<256>(mx, mb, mo, p, t256.n_tiles, st);
+  if (t128.cost <= t64.cost) return latent_project_launch<128>(mx, mb, mo, p, t128.n_tiles, st);
+  return latent_project_launch<64>(mx, mb, mo, p, t64.n_tiles, st);
 }
 
 s4r_status s4r_prefill_attend(const s4r_prefill_attend_args *a, void *stream) {
