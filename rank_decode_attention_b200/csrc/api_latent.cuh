@@ -49,7 +49,7 @@ s4r_status latent_attend_shape(const s4r_latent_attend_args *a) {
 // Blocks of query rows, grid and workspace of a latent attention call.
 struct LatentPlan {
   int nb, row_blocks, n_ctas;
-  size_t flags, units, ml, part, total;
+  size_t unit_poison, part_poison, units, ml, part, total;
 };
 LatentPlan latent_plan(const s4r_latent_attend_args *a) {
   LatentPlan l;
@@ -59,8 +59,10 @@ LatentPlan latent_plan(const s4r_latent_attend_args *a) {
   const int64_t tiles = (int64_t)a->batch * l.row_blocks * ceil_div((int64_t)a->max_pages * a->page_size, kLaTile);
   l.n_ctas = (int)smax<int64_t>(1, smin<int64_t>(tiles, sm_count()));
   size_t off = kAlign;   // status word
-  l.flags = off;
+  l.unit_poison = off;
   off += round_up(sizeof(int32_t) * (size_t)a->batch * l.row_blocks);
+  l.part_poison = off;
+  off += round_up(sizeof(int32_t) * 2 * (size_t)l.n_ctas);
   l.units = off;
   off += round_up(sizeof(int2) * (size_t)a->batch * l.row_blocks);
   l.ml = off;
@@ -248,7 +250,8 @@ s4r_status s4r_latent_attend(const s4r_latent_attend_args *a, void *stream) {
   p.n_ctas = l.n_ctas;
   p.slots = la_layout(l.nb, a->width, fp4).slots;
   p.status = reinterpret_cast<uint32_t *>(ws);
-  p.flags = reinterpret_cast<int32_t *>(ws + l.flags);
+  p.unit_poison = reinterpret_cast<int32_t *>(ws + l.unit_poison);
+  p.part_poison = reinterpret_cast<int32_t *>(ws + l.part_poison);
   p.units = reinterpret_cast<int2 *>(ws + l.units);
   p.ml = reinterpret_cast<float2 *>(ws + l.ml);
   p.part = reinterpret_cast<float *>(ws + l.part);
@@ -327,7 +330,7 @@ s4r_status s4r_prefill_attend(const s4r_prefill_attend_args *a, void *stream) {
       a->n_heads_q % a->n_heads_kv)
     return S4R_ERR_INVALID_ARG;
   if (a->head_dim % 8 || a->rope_dim % 8 || a->value_dim % 8 || a->head_dim > 128 || a->value_dim > 128 ||
-      a->rope_dim > 64 || a->batch > 65535 || a->n_heads_q > 65535 || a->total_q > INT32_MAX || a->total_k > INT32_MAX)
+      a->rope_dim > 64 || a->batch > 65535 || a->n_heads_q > 65535 || a->max_q > 65535 * 2 * kPfTile || a->total_q > INT32_MAX || a->total_k > INT32_MAX)
     return S4R_ERR_UNSUPPORTED;
   if (a->batch == 0 || a->total_q == 0 || a->max_q == 0) return S4R_OK;
   const void *must[] = {a->q, a->cu_q, a->cu_k, a->out};
@@ -346,7 +349,30 @@ s4r_status s4r_prefill_attend(const s4r_prefill_attend_args *a, void *stream) {
                   static_cast<const bf16 *>(a->v), static_cast<const bf16 *>(a->k_rope), a->k_ts, a->v_ts, a->k_rope_ts,
                   a->cu_q, a->cu_k, static_cast<bf16 *>(a->out), a->lse};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  prefill_attend_simt<<<dim3((unsigned)ceil_div(a->max_q, 8), (unsigned)a->n_heads_q, (unsigned)a->batch), 256, 0, st>>>(p);
+  const int chunks = pf_key_chunks(a->head_dim, a->rope_dim);
+  // Tensors without rows, or without a rotary part, are never loaded.
+  const bf16 *k = keys ? p.k : p.q, *v = keys ? p.v : p.q, *kr = keys && a->rope_dim > 0 ? p.k_rope : p.q;
+  const uint64_t nk = keys ? (uint64_t)a->total_k : 1, q_row = (uint64_t)(a->head_dim + a->rope_dim) * 2;
+  auto map3 = [](CUtensorMap *m, const bf16 *ptr, int64_t n, int64_t heads, uint64_t rows, uint64_t head_bytes, uint64_t row_bytes) {
+    const uint64_t d[3] = {(uint64_t)n, (uint64_t)heads, rows}, st[2] = {head_bytes, row_bytes};
+    const uint32_t box[3] = {64, 1, kPfTile};
+    return make_tmap_bf16_nd(m, ptr, 3, d, st, box);
+  };
+  CUtensorMap mq, mqr, mk, mkr, mv;
+  const int64_t rd = a->rope_dim > 0 ? a->rope_dim : 8;
+  if (!map3(&mq, p.q, a->head_dim, a->n_heads_q, a->total_q, q_row, q_row * a->n_heads_q) ||
+      !map3(&mqr, a->rope_dim > 0 ? p.q + a->head_dim : p.q, rd, a->n_heads_q, a->total_q, q_row, q_row * a->n_heads_q) ||
+      !map3(&mk, k, a->head_dim, keys ? a->n_heads_kv : 1, nk, (uint64_t)a->head_dim * 2, keys ? (uint64_t)a->k_ts * 2 : 16) ||
+      !map3(&mkr, kr, rd, 1, keys && a->rope_dim > 0 ? nk : 1, 16, keys && a->rope_dim > 0 ? (uint64_t)a->k_rope_ts * 2 : 16) ||
+      !map3(&mv, v, a->value_dim, keys ? a->n_heads_kv : 1, nk, (uint64_t)a->value_dim * 2, keys ? (uint64_t)a->v_ts * 2 : 16)) {
+    snprintf(g_last_error, sizeof(g_last_error), "cuTensorMapEncodeTiled failed for s4r_prefill_attend");
+    return S4R_ERR_CUDA;
+  }
+  const size_t smem = pf_smem_bytes(chunks);
+  const cudaError_t err = ensure_smem<prefill_attend_kernel>(smem);
+  if (err != cudaSuccess) return fail("prefill_attend_kernel (shared memory)", err);
+  const dim3 grid((unsigned)a->n_heads_q, (unsigned)a->batch, (unsigned)ceil_div(a->max_q, 2 * kPfTile));
+  prefill_attend_kernel<<<grid, kPfThreads, smem, st>>>(mq, mqr, mk, mkr, mv, p);
   return check_launch("prefill_attend");
 }
 

@@ -75,7 +75,9 @@ struct LatentAttend {
   int32_t rows, row_blocks, n_ctas, slots;   // query rows a request, blocks of NB of them, grid, ring slots
   // workspace
   uint32_t *status;
-  int32_t *flags;                            // [batch * row_blocks] recompute the unit (see latent_combine_kernel)
+  // first row with a value that some query rows must not see (see latent_combine_kernel), INT32_MAX for none: of a
+  // unit that one CTA computes whole, of a part
+  int32_t *unit_poison, *part_poison;        // [batch * row_blocks], [2 * n_ctas]
   int2 *units;                               // [batch * row_blocks] first part, and how many (1: computed whole)
   float2 *ml;                                // [2 * n_ctas][NB] reference maximum and sum of a partial
   float *part;                               // [2 * n_ctas][NB][rank] unscaled partial results
@@ -121,6 +123,7 @@ struct LaControl {
   int fail;   // a wait of the softmax warps gave up
   int first_b, first_off, n_tiles;   // start of this CTA's range and its length
   int share;                         // tiles of a full range
+  int poison[kLaSoftmaxWarps];
   int16_t qexp[2][64];               // 4-bit cache: queries are scaled by 2^qexp (segments alternate)
   alignas(8) float wmax[4][64];
   float fac[64];
@@ -220,6 +223,10 @@ __device__ __forceinline__ void la_bar(int id) {
   __syncwarp();
   asm volatile("barrier.cta.sync.aligned %0, 128;" ::"r"(id) : "memory");
 }
+__device__ __forceinline__ void la_bar_all() {   // both groups
+  __syncwarp();
+  asm volatile("barrier.cta.sync.aligned 3, %0;" ::"n"(kLaSoftmaxWarps * 32) : "memory");
+}
 __device__ __forceinline__ bool la_bar_any(int id, bool x) {
   uint32_t r;
   __syncwarp();
@@ -236,17 +243,6 @@ __device__ __forceinline__ bool la_bar_any(int id, bool x) {
 __device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return (uint32_t)__half_as_ushort(__low2half(h)) | ((uint32_t)__half_as_ushort(__high2half(h)) << 16);
-}
-
-// Whether any of eight 16-bit floats is infinite or NaN (all exponent bits set).
-template <bool FP4>
-__device__ __forceinline__ bool la_not_finite(const uint4 &v) {
-  const uint32_t e = FP4 ? 0x7c00u : 0x7f80u;
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-  bool bad = false;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) bad |= (w[i] & e) == e || ((w[i] >> 16) & e) == e;
-  return bad;
 }
 
 template <int NB, bool FP4>
@@ -536,7 +532,7 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_co
         if (p.lse)
           for (int i = tid; i < p.rows; i += 128) p.lse[(int64_t)b * p.rows + i] = -CUDART_INF_F;
         for (int i = tid; i < p.row_blocks; i += 128) {
-          p.flags[b * p.row_blocks + i] = 0;
+          p.unit_poison[b * p.row_blocks + i] = INT32_MAX;
           p.units[b * p.row_blocks + i] = make_int2(0, 1);
         }
       }
@@ -555,7 +551,7 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_co
         mul[i] = to2;
       }
       const int all_see = s.len - p.n_query + 1;   // tokens that every query row sees
-      bool poison = false;
+      int poison = INT32_MAX;
       for (int j = s.tile; j < s.tile + s.n; ++j, ++n) {
         const uint32_t buf = n & 1;
         if (!mbar_wait_within(&ctl->s_full[buf], (n >> 1) & 1, limit, p.status)) ctl->fail = 1;
@@ -600,8 +596,8 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_co
         if (edge) {
           // Rows behind the length hold anything: their probabilities are 0,
           // and so must they be.  Rows that some query rows see and others do
-          // not must be finite, or the unit is computed again by the combine
-          // kernel.
+          // not must be finite, too: what is not becomes 0, and the query rows
+          // that see it are computed again by the combine kernel.
           const int valid = smin(s.len - j * kLaTile, kLaTile), shared_rows = smax(all_see - j * kLaTile, 0);
           LaRing at = slot;
           for (int k = 0; k < pairs; ++k, at.step(n_slots)) {
@@ -614,9 +610,10 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_co
               if (h == grp || halves == 1)   // a single half by both
                 for (int i = valid * 8 + tid; i < kLaTile * 8; i += 128)
                   *reinterpret_cast<uint4 *>(half + i * 16) = make_uint4(0u, 0u, 0u, 0u);
-              if (p.n_query > 1 && grp == 0)
+              if (p.n_query > 1 && (h == grp || halves == 1))
                 for (int i = shared_rows * 8 + tid; i < valid * 8; i += 128)
-                  poison |= la_not_finite<FP4>(*reinterpret_cast<const uint4 *>(half + i * 16));
+                  if (clear_not_finite<FP4 ? 0x7c00u : 0x7f80u>(*reinterpret_cast<uint4 *>(half + i * 16)))
+                    poison = smin(poison, j * kLaTile + (i >> 3));
             }
           }
         }
@@ -723,12 +720,17 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_co
         const int rest = s.unit_tiles - s.n, share = ctl->share;
         p.units[s.b * p.row_blocks + s.rb] = make_int2(part, 1 + (rest + share - 1) / share);
       }
-      if (p.n_query > 1 && s.tile + s.n == s.unit_tiles) {
-        const bool any = la_bar_any(bar, poison);
-        if (tid == 0 && grp == 0) p.flags[s.b * p.row_blocks + s.rb] = any ? 1 : 0;
-      } else {
-        la_bar(bar);
+      if (p.n_query > 1) {
+        // each group has looked at one half of the columns
+        poison = __reduce_min_sync(0xffffffffu, poison);
+        if (lane == 0) ctl->poison[warp - 2] = poison;
+        la_bar_all();
+        if (tid == 0 && grp == 0) {
+          for (int w = 1; w < kLaSoftmaxWarps; ++w) poison = smin(poison, ctl->poison[w]);
+          (whole ? p.unit_poison[s.b * p.row_blocks + s.rb] : p.part_poison[part]) = poison;
+        }
       }
+      la_bar(bar);
       if (!mbar_wait_within(&ctl->pv_done, (n - 1) & 1, limit, p.status)) ctl->fail = 1;
       __syncwarp();
       tc_fence_after();
@@ -871,10 +873,10 @@ __device__ __forceinline__ float latent_value(const LatentAttend &p, int64_t pag
 // Joins the partial sums of one query row (and of `cols` columns, a multiple
 // of 128 that is less than the rank when there are few rows), a CTA each:
 //   out = sum_k 2^(m_k - m) O_k / sum_k 2^(m_k - m) l_k, m = max_k m_k.
-// Units that one CTA computed whole are skipped.  A unit whose flag is set
-// (rows that only some of its query rows see hold infinities or NaN, which a
-// probability of 0 would not hide from the others in a matrix product) is
-// computed again here, row by row over the rows it sees: rare, and slow.
+// Units that one CTA computed whole are skipped.  Query rows that see an
+// infinity or a NaN which other rows of the request must not see (the products
+// took it as 0) are computed again here, row by row over the cache: rare, and
+// slow.
 constexpr int kLcThreads = 128;
 template <int NB, bool FP4>
 __global__ void __launch_bounds__(kLcThreads) latent_combine_kernel(const LatentAttend p, const int cols) {
@@ -886,9 +888,15 @@ __global__ void __launch_bounds__(kLcThreads) latent_combine_kernel(const Latent
   const int2 parts = p.units[unit];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   constexpr int W = kLcThreads / 32, kCols = S4R_MAX_LATENT_RANK / 32;
-  if (p.n_query > 1 && p.flags[unit]) {
+  const int sees = la_length(p, b) - p.n_query + 1 + row / p.n_heads;
+  int poison = INT32_MAX;
+  if (p.n_query > 1) {
+    if (parts.y <= 1) poison = p.unit_poison[unit];
+    else
+      for (int i = 0; i < parts.y; ++i) poison = smin(poison, p.part_poison[i == 0 ? parts.x : 2 * (parts.x / 2 + i)]);
+  }
+  if (sees > poison) {
     if (blockIdx.y > 0) return;
-    const int sees = la_length(p, b) - p.n_query + 1 + row / p.n_heads;
     float m = -CUDART_INF_F, l = 0.0f, acc[kCols];
 #pragma unroll
     for (int k = 0; k < kCols; ++k) acc[k] = 0.0f;

@@ -1,4 +1,28 @@
-// k_prefill.cuh -- causal attention of ragged prompts over expanded keys and values.
+// k_prefill.cuh -- attention of ragged prompts over expanded keys and values.
+//
+// S = scale (q . k + q_rope . k_rope), P = softmax(S) with a causal limit a
+// row, O = P V: bound by the tensor cores (320 multiply-adds a query, key and
+// head at 128 + 64 | 128, and one exponential).
+//
+// A CTA takes 256 queries of one head as two tiles of 128 and walks along the
+// keys in tiles of 128.  While the softmax of one query tile runs, the tensor
+// cores work for the other one.  TMEM holds S and O of both tiles (4 x 128
+// columns); P, in bf16, replaces the S it comes from and is the first operand
+// of the second product straight from TMEM, so shared memory holds queries,
+// keys and values only.
+//   warp 0     loads with TMA: the queries once, then K and V in 128 x 64
+//              chunks through a ring.  In key tiles that end behind the
+//              sequence it clears the rows of V behind the end, and in tiles on
+//              the diagonal it looks for infinities and NaN among values that
+//              some rows must not see (a probability of 0 would not hide them):
+//              if there are any, the rows are computed again one by one at the
+//              end;
+//   warp 1     issues tcgen05.mma;
+//   warps 2-9  softmax, a thread a query: the reference maximum moves only when
+//              a logit exceeds it by more than 2^8 (then the thread rescales its
+//              row of O), so no thread waits for another one.
+// CTAs start with the queries that see most keys, all heads of them, so that
+// the short ones fill up the end.
 #pragma once
 #include <math_constants.h>
 
@@ -17,6 +41,13 @@ struct PrefillAttend {
   float *lse;
 };
 
+constexpr int kPfTile = 128;                     // queries a tile, keys a tile
+constexpr int kPfChunk = kPfTile * 128;          // bytes of 128 rows x 64 columns
+constexpr int kPfThreads = 320;
+constexpr int kPfMaxSlots = 12;
+constexpr int kPfControlBytes = 1024;
+constexpr float kPfLift = 8.0f;
+
 // Rows of sequence b (false, and the library-wide status set, if its offsets
 // are not within the tensors).
 struct PrefillSeq {
@@ -32,17 +63,51 @@ __device__ __forceinline__ bool prefill_seq(const PrefillAttend &p, int b, Prefi
   return q0 >= 0 && q1 >= q0 && q1 <= p.total_q && k0 >= 0 && k1 >= k0 && k1 <= p.total_k;
 }
 
-// One warp a (query, head): keys one after another with a running maximum and sum.
-__global__ void __launch_bounds__(256) prefill_attend_simt(const PrefillAttend p) {
-  const int lane = threadIdx.x & 31, h = blockIdx.y, b = blockIdx.z;
-  const int32_t i = (int32_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  PrefillSeq s;
-  if (!prefill_seq(p, b, s)) {
-    set_status(&g_device_status, kDevStatusCheck);
-    return;
+// Chunks of a key (and query) row, of a value row, and ring slots that fit.
+__host__ __device__ inline int pf_key_chunks(int dim, int rope) { return (dim + 63) / 64 + (rope + 63) / 64; }
+__host__ __device__ inline int pf_slots(int key_chunks) {
+  return smin((227 * 1024 - 1024 - kPfControlBytes - 2 * key_chunks * kPfChunk) / kPfChunk, kPfMaxSlots);
+}
+__host__ inline size_t pf_smem_bytes(int key_chunks) {
+  return (size_t)(2 * key_chunks + pf_slots(key_chunks)) * kPfChunk + kPfControlBytes + 1024;
+}
+
+struct PfControl {
+  uint64_t full[kPfMaxSlots], empty[kPfMaxSlots];
+  uint64_t q_full, landed;
+  uint64_t s_full[2], p_full[2], pv_done[2];
+  uint32_t tmem_base;
+  int poison;   // first key whose values some rows must not see
+};
+static_assert(sizeof(PfControl) <= kPfControlBytes, "control block");
+
+struct PfRing {
+  int st = 0;
+  uint32_t turn = 0;
+  __device__ __forceinline__ void step(int n) {
+    if (++st == n) {
+      st = 0;
+      ++turn;
+    }
   }
-  if (s.nq > p.max_q) set_status(&g_device_status, kDevStatusCheck);
-  if (i >= smin(s.nq, p.max_q)) return;
+};
+
+// D[tmem] (+)= A[tmem] * B[smem desc], kind::f16, under a predicate.
+__device__ __forceinline__ void umma_f16_ts_if(uint32_t on, uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                               bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"((uint32_t)accumulate), "r"(on)
+      : "memory");
+}
+
+// One query row by one warp, keys one after another: the rows of a CTA that
+// met infinities where only some of its rows may see them.
+__device__ __noinline__ void prefill_row(const PrefillAttend &p, const PrefillSeq &s, int i, int h) {
+  const int lane = threadIdx.x & 31;
   const int32_t g = h / (p.hq / p.hkv);
   const bf16 *q = p.q + ((s.q0 + i) * p.hq + h) * (int64_t)(p.dim + p.rope);
   float qv[4], qr[2], acc[4];
@@ -79,6 +144,338 @@ __global__ void __launch_bounds__(256) prefill_attend_simt(const PrefillAttend p
   for (int c = 0; c < 4; ++c)
     if (lane + 32 * c < p.vdim) o[lane + 32 * c] = from_f<bf16>(sees > 0 ? acc[c] / l : 0.0f);
   if (lane == 0 && p.lse) p.lse[(s.q0 + i) * p.hq + h] = sees > 0 ? m + logf(l) : -CUDART_INF_F;
+}
+
+__global__ void __launch_bounds__(kPfThreads, 1)
+prefill_attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_qr,
+                      const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_kr,
+                      const __grid_constant__ CUtensorMap map_v, const PrefillAttend p) {
+  extern __shared__ __align__(1024) unsigned char pf_smem_raw[];
+  unsigned char *smem = reinterpret_cast<unsigned char *>(
+      (reinterpret_cast<uintptr_t>(pf_smem_raw) + 1023) & ~uintptr_t(1023));
+  const int nope = (p.dim + 63) / 64, kc = pf_key_chunks(p.dim, p.rope), vc = (p.vdim + 63) / 64, n_slots = pf_slots(kc);
+  unsigned char *ring = smem + 2 * kc * kPfChunk;
+  PfControl *ctl = reinterpret_cast<PfControl *>(ring + n_slots * kPfChunk);
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const int h = blockIdx.x, b = blockIdx.y, q0 = (int)(gridDim.z - 1 - blockIdx.z) * 2 * kPfTile;
+  const int g = h / (p.hq / p.hkv);
+  PrefillSeq s;
+  if (!prefill_seq(p, b, s)) {   // the same in every thread
+    if (threadIdx.x == 0) set_status(&g_device_status, kDevStatusCheck);
+    return;
+  }
+  if (s.nq > p.max_q && threadIdx.x == 0) set_status(&g_device_status, kDevStatusCheck);
+  const int rows = smin(s.nq, p.max_q);   // rows to compute
+  if (q0 >= rows) return;
+  // Key tiles of each query tile: up to what its last row sees.
+  int n_t[2];
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const int last = smin(q0 + (t + 1) * kPfTile, rows) - 1;
+    const int64_t sees = last < q0 + t * kPfTile ? 0 : p.causal ? smin<int64_t>((int64_t)s.nk - s.nq + last + 1, s.nk) : s.nk;
+    n_t[t] = sees > 0 ? (int)((sees + kPfTile - 1) / kPfTile) : 0;
+  }
+  const int n_all = smax(n_t[0], n_t[1]);
+  const long long limit = wait_limit();
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < n_slots; ++i) {
+      mbar_init(&ctl->full[i], 1);
+      mbar_init(&ctl->empty[i], 1);
+    }
+    mbar_init(&ctl->q_full, 1);
+    mbar_init(&ctl->landed, 1);
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&ctl->s_full[t], 1);
+      mbar_init(&ctl->p_full[t], 4);
+      mbar_init(&ctl->pv_done[t], 1);
+    }
+    mbar_fence_init();
+    ctl->poison = INT32_MAX;
+  }
+  if (warp == 0) tmem_alloc(&ctl->tmem_base, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, ctl->tmem_base, 0);
+  auto wait = [&](uint64_t *bar, uint32_t parity) {
+    return __shfl_sync(0xffffffffu, (int)mbar_wait_within(bar, parity & 1, limit, nullptr), 0) != 0;
+  };
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    const uint32_t leader = elect_one();
+    bool ok = n_all > 0;
+    PfRing slot;
+    uint32_t touched = 0;
+    if (ok) {
+      mbar_expect_if(leader, &ctl->q_full, (uint32_t)(2 * kc) * kPfChunk);
+      for (int t = 0; t < 2; ++t)
+        for (int c = 0; c < kc; ++c) {
+          const int row = (int)s.q0 + q0 + t * kPfTile;
+          unsigned char *dst = smem + (t * kc + c) * kPfChunk;
+          if (c < nope) tma_load_3d_if(leader, dst, &map_q, &ctl->q_full, c * 64, h, row);
+          else tma_load_3d_if(leader, dst, &map_qr, &ctl->q_full, (c - nope) * 64, h, row);
+        }
+    }
+    for (int j = 0; j < n_all && ok; ++j) {
+      const int row = (int)s.k0 + j * kPfTile;
+      for (int c = 0; c < kc && ok; ++c, slot.step(n_slots)) {
+        if (slot.turn > 0) ok = wait(&ctl->empty[slot.st], slot.turn - 1);
+        if (!ok) break;
+        mbar_expect_if(leader, &ctl->full[slot.st], kPfChunk);
+        if (c < nope) tma_load_3d_if(leader, ring + slot.st * kPfChunk, &map_k, &ctl->full[slot.st], c * 64, g, row);
+        else tma_load_3d_if(leader, ring + slot.st * kPfChunk, &map_kr, &ctl->full[slot.st], (c - nope) * 64, 0, row);
+      }
+      if (ok && vc == 2 && slot.st == n_slots - 1) {   // the two chunks of V lie side by side: skip the last slot
+        if (slot.turn > 0) ok = wait(&ctl->empty[slot.st], slot.turn - 1);
+        if (ok && leader) mbar_arrive(&ctl->full[slot.st]);
+        slot.step(n_slots);
+      }
+      // Rows of V behind the end of the sequence; rows that not every query sees.
+      const int live = smin(s.nk - j * kPfTile, kPfTile);
+      const int64_t all_see = p.causal ? (int64_t)s.nk - s.nq + q0 + 1 - (int64_t)j * kPfTile : kPfTile;
+      const bool touch = live < kPfTile || all_see < live;
+      PfRing first = slot;
+      if (ok && touch) mbar_expect_if(leader, &ctl->landed, (uint32_t)vc * kPfChunk);
+      for (int c = 0; c < vc && ok; ++c, slot.step(n_slots)) {
+        if (slot.turn > 0) ok = wait(&ctl->empty[slot.st], slot.turn - 1);
+        if (!ok) break;
+        if (!touch) mbar_expect_if(leader, &ctl->full[slot.st], kPfChunk);
+        tma_load_3d_if(leader, ring + slot.st * kPfChunk, &map_v, touch ? &ctl->landed : &ctl->full[slot.st], c * 64, g, row);
+      }
+      if (ok && touch) {
+        ok = wait(&ctl->landed, touched++);
+        if (!ok) break;
+        int bad = INT32_MAX;
+        const int from = (int)smax<int64_t>(all_see, 0);
+        for (int c = 0; c < vc; ++c) {
+          unsigned char *chunk = ring + (first.st + c) * kPfChunk;
+          for (int i = from * 8 + lane; i < live * 8; i += 32) {
+            uint4 *at = reinterpret_cast<uint4 *>(chunk + i * 16);
+            if (clear_not_finite<0x7f80u>(*at)) bad = smin(bad, j * kPfTile + (i >> 3));
+          }
+          for (int i = live * 8 + lane; i < kPfTile * 8; i += 32)
+            *reinterpret_cast<uint4 *>(chunk + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        if (bad != INT32_MAX) atomicMin(&ctl->poison, bad);
+        fence_async_smem();
+        __syncwarp();
+        if (leader)
+          for (int c = 0; c < vc; ++c) mbar_arrive(&ctl->full[first.st + c]);
+        __syncwarp();
+      }
+    }
+  } else if (warp == 1) {
+    // ---------------------------------------------------------- MMA issuer
+    const uint32_t leader = elect_one();
+    const uint32_t id_s = idesc_bf16_f32(128, 128, 0, 0), id_o = idesc_bf16_f32(128, 64 * vc, 0, 1);
+    const uint64_t q_desc = sdesc_sw128(smem_u32(smem), 16, 1024), k_desc = sdesc_sw128(smem_u32(ring), 16, 1024);
+    const uint64_t v_desc = sdesc_sw128(smem_u32(ring), kPfChunk, 1024);
+    bool ok = n_all > 0 && wait(&ctl->q_full, 0);
+    PfRing kp, vp;   // first slots of the key tile and of the value tile in turn
+    // S of query tile t and the key tile at kp; the slots are free after the last query tile
+    auto scores = [&](int t, bool last) {
+      PfRing at = kp;
+      const uint32_t d = tmem + t * 128;
+      for (int c = 0; c < kc; ++c, at.step(n_slots)) {
+        if (!wait(&ctl->full[at.st], at.turn)) return false;
+        tc_fence_after();
+        const uint64_t a = q_desc + (uint32_t)(t * kc + c) * (kPfChunk >> 4), k = k_desc + (uint32_t)at.st * (kPfChunk >> 4);
+        umma_f16_if(leader, d, a, k, id_s, c > 0);
+#pragma unroll
+        for (int ks = 1; ks < 4; ++ks) umma_f16_if(leader, d, a + ks * 2, k + ks * 2, id_s, true);
+        if (last) umma_commit_if(leader, &ctl->empty[at.st]);
+      }
+      umma_commit_if(leader, &ctl->s_full[t]);
+      return true;
+    };
+    auto values = [&](int t, int j, bool last) {
+      if (!wait(&ctl->p_full[t], (uint32_t)j)) return false;
+      for (int c = 0; c < vc; ++c)
+        if (!wait(&ctl->full[vp.st + c], vp.turn)) return false;
+      tc_fence_after();
+      const uint64_t v = v_desc + (uint32_t)vp.st * (kPfChunk >> 4);
+      const uint32_t d = tmem + 256 + t * 128, a = tmem + t * 128;
+#pragma unroll
+      for (int ks = 0; ks < kPfTile / 16; ++ks) umma_f16_ts_if(leader, d, a + ks * 8, v + ks * (2048 >> 4), id_o, ks > 0 || j > 0);
+      if (last)
+        for (int c = 0; c < vc; ++c) umma_commit_if(leader, &ctl->empty[vp.st + c]);
+      umma_commit_if(leader, &ctl->pv_done[t]);
+      return true;
+    };
+    // The value tile behind the key tile at kp, then the next key tile.
+    auto to_values = [&]() {
+      vp = kp;
+      for (int c = 0; c < kc; ++c) vp.step(n_slots);
+      if (vc == 2 && vp.st == n_slots - 1) {
+        const bool r = wait(&ctl->full[vp.st], vp.turn);
+        umma_commit_if(leader, &ctl->empty[vp.st]);
+        vp.step(n_slots);
+        return r;
+      }
+      return true;
+    };
+    if (ok && n_t[0] > 0) ok = scores(0, n_t[1] == 0);
+    if (ok && n_t[1] > 0) ok = scores(1, true);
+    for (int j = 0; j < n_all && ok; ++j) {
+      ok = to_values();
+      kp = vp;
+      for (int c = 0; c < vc; ++c) kp.step(n_slots);
+      if (ok && j < n_t[0]) ok = values(0, j, j >= n_t[1]);
+      if (ok && j + 1 < n_t[0]) ok = scores(0, j + 1 >= n_t[1]);
+      if (ok && j < n_t[1]) ok = values(1, j, true);
+      if (ok && j + 1 < n_t[1]) ok = scores(1, true);
+    }
+  } else {
+    // ------------------------------------------------------------- softmax
+    const int t = (warp - 2) >> 2, quad = warp & 3;
+    const int i = q0 + t * kPfTile + quad * 32 + lane;   // the thread's query
+    const uint32_t lanes = (uint32_t)(quad * 32) << 16;
+    const uint32_t s_at = tmem + lanes + t * 128, o_at = tmem + lanes + 256 + t * 128;
+    const int64_t last64 = p.causal ? smin<int64_t>((int64_t)s.nk - s.nq + i, s.nk - 1) : s.nk - 1;
+    const int last = (int)smax<int64_t>(last64, -1);     // the last key it sees
+    const float to2 = fabsf(p.scale) * 1.4426950408889634f;
+    const uint32_t flip = p.scale < 0.0f ? 0x80000000u : 0u;
+    float m = -CUDART_INF_F, l = 0.0f;
+    bool ok = true;
+    for (int j = 0; j < n_t[t]; ++j) {
+      ok = wait(&ctl->s_full[t], (uint32_t)j);
+      if (!ok) break;
+      tc_fence_after();
+      // Twice over the row: the maximum from the upper half and the lower one,
+      // then the probabilities from the lower half, still in registers, and the
+      // upper one, loaded again (P overwrites only what has been read).  All 128
+      // at once would not fit the 168 registers a thread has.
+      const int left = last - j * kPfTile;   // columns up to this one are seen
+      const bool cut = __any_sync(0xffffffffu, left < kPfTile - 1);
+      auto fix = [&](uint32_t (&x)[32], int c0) {   // sign of the scale, unseen columns
+        if (flip) {
+#pragma unroll
+          for (int c = 0; c < 32; ++c) x[c] ^= 0x80000000u;
+        }
+        if (cut) {
+#pragma unroll
+          for (int c = 0; c < 32; ++c)
+            if (c0 + c > left) x[c] = 0xff800000u;
+        }
+      };
+      float top[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
+      auto largest = [&](const uint32_t (&x)[32]) {
+#pragma unroll
+        for (int c = 0; c < 32; ++c) top[c & 3] = fmaxf(top[c & 3], __uint_as_float(x[c]));
+      };
+      uint32_t v0[32], v1[32];
+      tmem_ld32(s_at + 64, v0);
+      tmem_ld32(s_at + 96, v1);
+      tmem_wait_ld();
+      fix(v0, 64);
+      fix(v1, 96);
+      largest(v0);
+      largest(v1);
+      tmem_ld32(s_at, v0);
+      tmem_ld32(s_at + 32, v1);
+      tmem_wait_ld();
+      fix(v0, 0);
+      fix(v1, 32);
+      largest(v0);
+      largest(v1);
+      const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+      // -inf (nothing seen) stays so even at scale 0
+      const float y = most == -CUDART_INF_F ? most : most * to2;
+      if (__any_sync(0xffffffffu, y > m + kPfLift)) {
+        const float mn = fmaxf(m, y), f = mn == m ? 1.0f : exp2f(m - mn);
+        m = mn;
+        l *= f;
+        if (j > 0) {
+          ok = wait(&ctl->pv_done[t], (uint32_t)(j - 1));
+          if (!ok) break;
+          tc_fence_after();
+          for (int c = 0; c < 64 * vc; c += 32) {
+            uint32_t w[32];
+            tmem_ld32(o_at + c, w);
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 32; ++k) w[k] = __float_as_uint(__uint_as_float(w[k]) * f);
+            tmem_st32(o_at + c, w);
+          }
+        }
+      }
+      const float ref = m == -CUDART_INF_F ? 0.0f : m;
+      float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      auto exps = [&](const uint32_t (&x)[32], int c) {   // P of columns 32 c ..
+        uint32_t w[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const uint32_t r0 = x[2 * k], r1 = x[2 * k + 1];
+          float a = fmaf(__uint_as_float(r0), to2, -ref), e = fmaf(__uint_as_float(r1), to2, -ref);
+          if (to2 == 0.0f) {   // 0 x -inf
+            a = r0 == 0xff800000u ? -CUDART_INF_F : a;
+            e = r1 == 0xff800000u ? -CUDART_INF_F : e;
+          }
+          a = ex2_approx(a);
+          e = ex2_approx(e);
+          sum[k & 3] += a + e;
+          w[k] = pack_bf16(a, e);
+        }
+        tmem_st16(s_at + 16 * c, w);
+      };
+      exps(v0, 0);
+      tmem_ld32(s_at + 64, v0);
+      exps(v1, 1);
+      tmem_wait_ld();
+      tmem_ld32(s_at + 96, v1);
+      fix(v0, 64);
+      exps(v0, 2);
+      tmem_wait_ld();
+      fix(v1, 96);
+      exps(v1, 3);
+      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->p_full[t]);
+    }
+    if (ok && n_t[t] > 0) ok = wait(&ctl->pv_done[t], (uint32_t)(n_t[t] - 1));
+    tc_fence_after();
+    if (ok) {
+      const int64_t at = (s.q0 + i) * p.hq + h;
+      const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;   // a row that sees no key: 0
+      bf16 *o = p.out + at * p.vdim;
+      for (int c = 0; c < 64 * vc; c += 32) {
+        uint32_t w[32];
+        if (n_t[t] > 0) {
+          tmem_ld32(o_at + c, w);
+          tmem_wait_ld();
+        } else {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) w[k] = 0u;
+        }
+        if (i < rows) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (c + 8 * k < p.vdim) {
+              uint32_t r[4];
+#pragma unroll
+              for (int x = 0; x < 4; ++x)
+                r[x] = inv == 0.0f ? 0u : pack_bf16(__uint_as_float(w[8 * k + 2 * x]) * inv, __uint_as_float(w[8 * k + 2 * x + 1]) * inv);
+              *reinterpret_cast<uint4 *>(o + c + 8 * k) = make_uint4(r[0], r[1], r[2], r[3]);
+            }
+        }
+        __syncwarp();
+      }
+      if (i < rows && p.lse) p.lse[at] = l == 0.0f ? -CUDART_INF_F : (m + log2f(l)) * 0.6931471805599453f;
+      const int poison = *reinterpret_cast<volatile int *>(&ctl->poison);
+      if (poison != INT32_MAX)
+        for (int r = 0; r < 32; ++r) {
+          const int row = q0 + t * kPfTile + quad * 32 + r;
+          if (row < rows && (int64_t)s.nk - s.nq + row >= poison) prefill_row(p, s, row, h);
+        }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) tmem_dealloc(tmem, 512);
 }
 
 }  // namespace s4r

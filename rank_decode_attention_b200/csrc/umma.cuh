@@ -379,4 +379,31 @@ template <int N> __device__ __forceinline__ void bulk_wait_read() {
   asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
 }
 
+// Store 16 consecutive 32-bit columns of the warp's 32 lanes.
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(
+          taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+// Replace those of eight 16-bit floats that are infinite or NaN (all exponent
+// bits set) by 0, and say whether there were any.
+template <uint32_t EXPONENT>
+__device__ __forceinline__ bool clear_not_finite(uint4 &v) {
+  uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  bool any = false;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const bool lo = (w[i] & EXPONENT) == EXPONENT, hi = ((w[i] >> 16) & EXPONENT) == EXPONENT;
+    any |= lo || hi;
+    if (lo) w[i] &= 0xffff0000u;
+    if (hi) w[i] &= 0x0000ffffu;
+  }
+  if (any) v = make_uint4(w[0], w[1], w[2], w[3]);
+  return any;
+}
+
 }  // namespace s4r

@@ -333,7 +333,7 @@ def test_latent_attend_infinite_values_in_seen_rows(dt):
 
 
 @pytest.mark.parametrize("H", [5, 40])
-@pytest.mark.parametrize("n", [3, 64, 66, 20000])
+@pytest.mark.parametrize("n", [3, 64, 65, 66, 20000, 20033])
 def test_latent_attend_infinities_that_only_later_queries_see(n, H):
     """The newest row holds an infinity and the one before it a NaN in a value column: the queries that do not see them
     stay exact."""
