@@ -152,6 +152,17 @@ s4r_status latent_project_launch(const CUtensorMap &mx, const CUtensorMap &mb, c
   return check_launch("latent_project_kernel");
 }
 
+template <int KC, int VC>
+s4r_status prefill_launch(const CUtensorMap &mq, const CUtensorMap &mqr, const CUtensorMap &mk, const CUtensorMap &mkr,
+                          const CUtensorMap &mv, const PrefillAttend &p, cudaStream_t st) {
+  const size_t smem = pf_smem_bytes(KC);
+  const cudaError_t err = ensure_smem<prefill_attend_kernel<KC, VC>>(smem);
+  if (err != cudaSuccess) return fail("prefill_attend_kernel (shared memory)", err);
+  const dim3 grid((unsigned)p.hq, (unsigned)p.batch, (unsigned)ceil_div(p.max_q, 2 * kPfTile));
+  prefill_attend_kernel<KC, VC><<<grid, kPfThreads, smem, st>>>(mq, mqr, mk, mkr, mv, p);
+  return check_launch("prefill_attend_kernel");
+}
+
 }  // namespace
 
 extern "C" {
@@ -368,12 +379,15 @@ s4r_status s4r_prefill_attend(const s4r_prefill_attend_args *a, void *stream) {
     snprintf(g_last_error, sizeof(g_last_error), "cuTensorMapEncodeTiled failed for s4r_prefill_attend");
     return S4R_ERR_CUDA;
   }
-  const size_t smem = pf_smem_bytes(chunks);
-  const cudaError_t err = ensure_smem<prefill_attend_kernel>(smem);
-  if (err != cudaSuccess) return fail("prefill_attend_kernel (shared memory)", err);
-  const dim3 grid((unsigned)a->n_heads_q, (unsigned)a->batch, (unsigned)ceil_div(a->max_q, 2 * kPfTile));
-  prefill_attend_kernel<<<grid, kPfThreads, smem, st>>>(mq, mqr, mk, mkr, mv, p);
-  return check_launch("prefill_attend");
+  const int vc = (int)ceil_div(a->value_dim, 64);
+  auto launch = [&](auto kc_, auto vc_) { return prefill_launch<decltype(kc_)::value, decltype(vc_)::value>(mq, mqr, mk, mkr, mv, p, st); };
+  using std::integral_constant;
+  auto with_values = [&](auto kc_) {
+    return vc == 1 ? launch(kc_, integral_constant<int, 1>{}) : launch(kc_, integral_constant<int, 2>{});
+  };
+  return chunks == 1   ? with_values(integral_constant<int, 1>{})
+         : chunks == 2 ? with_values(integral_constant<int, 2>{})
+                       : with_values(integral_constant<int, 3>{});
 }
 
 }  // extern "C"

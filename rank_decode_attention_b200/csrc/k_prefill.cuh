@@ -65,8 +65,10 @@ __device__ __forceinline__ bool prefill_seq(const PrefillAttend &p, int b, Prefi
 
 // Chunks of a key (and query) row, of a value row, and ring slots that fit.
 __host__ __device__ inline int pf_key_chunks(int dim, int rope) { return (dim + 63) / 64 + (rope + 63) / 64; }
-__host__ __device__ inline int pf_slots(int key_chunks) {
-  return smin((227 * 1024 - 1024 - kPfControlBytes - 2 * key_chunks * kPfChunk) / kPfChunk, kPfMaxSlots);
+__host__ __device__ constexpr int pf_slots(int key_chunks) {
+  return (227 * 1024 - 1024 - kPfControlBytes - 2 * key_chunks * kPfChunk) / kPfChunk < kPfMaxSlots
+             ? (227 * 1024 - 1024 - kPfControlBytes - 2 * key_chunks * kPfChunk) / kPfChunk
+             : kPfMaxSlots;
 }
 __host__ inline size_t pf_smem_bytes(int key_chunks) {
   return (size_t)(2 * key_chunks + pf_slots(key_chunks)) * kPfChunk + kPfControlBytes + 1024;
@@ -74,7 +76,7 @@ __host__ inline size_t pf_smem_bytes(int key_chunks) {
 
 struct PfControl {
   uint64_t full[kPfMaxSlots], empty[kPfMaxSlots];
-  uint64_t q_full, landed;
+  uint64_t q_full, landed, drained;
   uint64_t s_full[2], p_full[2], pv_done[2];
   uint32_t tmem_base;
   int poison;   // first key whose values some rows must not see
@@ -146,6 +148,11 @@ __device__ __noinline__ void prefill_row(const PrefillAttend &p, const PrefillSe
   if (lane == 0 && p.lse) p.lse[(s.q0 + i) * p.hq + h] = sees > 0 ? m + logf(l) : -CUDART_INF_F;
 }
 
+// KC, VC: 64-column chunks of a key (rotary part included) and of a value; as
+// constants, since the issuing warp is bound by the instructions around its
+// products (one prompt of 8192 and 16 heads took 393 us with them as variables,
+// 368 us as constants).
+template <int KC, int VC>
 __global__ void __launch_bounds__(kPfThreads, 1)
 prefill_attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_qr,
                       const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_kr,
@@ -153,7 +160,8 @@ prefill_attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
   extern __shared__ __align__(1024) unsigned char pf_smem_raw[];
   unsigned char *smem = reinterpret_cast<unsigned char *>(
       (reinterpret_cast<uintptr_t>(pf_smem_raw) + 1023) & ~uintptr_t(1023));
-  const int nope = (p.dim + 63) / 64, kc = pf_key_chunks(p.dim, p.rope), vc = (p.vdim + 63) / 64, n_slots = pf_slots(kc);
+  constexpr int kc = KC, vc = VC, n_slots = pf_slots(KC);
+  const int nope = (p.dim + 63) / 64;
   unsigned char *ring = smem + 2 * kc * kPfChunk;
   PfControl *ctl = reinterpret_cast<PfControl *>(ring + n_slots * kPfChunk);
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -173,7 +181,8 @@ prefill_attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
   for (int t = 0; t < 2; ++t) {
     const int last = smin(q0 + (t + 1) * kPfTile, rows) - 1;
     const int64_t sees = last < q0 + t * kPfTile ? 0 : p.causal ? smin<int64_t>((int64_t)s.nk - s.nq + last + 1, s.nk) : s.nk;
-    n_t[t] = sees > 0 ? (int)((sees + kPfTile - 1) / kPfTile) : 0;
+    // broadcast, for the compiler to see that it is uniform
+    n_t[t] = __shfl_sync(0xffffffffu, sees > 0 ? (int)((sees + kPfTile - 1) / kPfTile) : 0, 0);
   }
   const int n_all = smax(n_t[0], n_t[1]);
   const long long limit = wait_limit();
@@ -185,6 +194,7 @@ prefill_attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
     }
     mbar_init(&ctl->q_full, 1);
     mbar_init(&ctl->landed, 1);
+    mbar_init(&ctl->drained, 1);
     for (int t = 0; t < 2; ++t) {
       mbar_init(&ctl->s_full[t], 1);
       mbar_init(&ctl->p_full[t], 4);
@@ -266,21 +276,29 @@ prefill_attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
         __syncwarp();
       }
     }
+    if (!ok && n_all > 0) {   // let the copies in flight land before the CTA ends
+      wait(&ctl->q_full, 0);
+      for (int i = 0; i < n_slots; ++i)
+        if (slot.turn > 0 || i < slot.st) wait(&ctl->full[i], slot.turn - (i < slot.st ? 0 : 1));
+    }
   } else if (warp == 1) {
     // ---------------------------------------------------------- MMA issuer
     const uint32_t leader = elect_one();
     const uint32_t id_s = idesc_bf16_f32(128, 128, 0, 0), id_o = idesc_bf16_f32(128, 64 * vc, 0, 1);
     const uint64_t q_desc = sdesc_sw128(smem_u32(smem), 16, 1024), k_desc = sdesc_sw128(smem_u32(ring), 16, 1024);
     const uint64_t v_desc = sdesc_sw128(smem_u32(ring), kPfChunk, 1024);
-    bool ok = n_all > 0 && wait(&ctl->q_full, 0);
+    bool ok = true;   // after a wait that gave up the others do not wait, and the walk ends
+    auto until = [&](uint64_t *bar, uint32_t parity) {
+      if (ok) ok = wait(bar, parity);
+      tc_fence_after();
+    };
     PfRing kp, vp;   // first slots of the key tile and of the value tile in turn
     // S of query tile t and the key tile at kp; the slots are free after the last query tile
-    auto scores = [&](int t, bool last) {
+    auto scores = [&](int t, bool first, bool last) {
       PfRing at = kp;
       const uint32_t d = tmem + t * 128;
       for (int c = 0; c < kc; ++c, at.step(n_slots)) {
-        if (!wait(&ctl->full[at.st], at.turn)) return false;
-        tc_fence_after();
+        if (first) until(&ctl->full[at.st], at.turn);
         const uint64_t a = q_desc + (uint32_t)(t * kc + c) * (kPfChunk >> 4), k = k_desc + (uint32_t)at.st * (kPfChunk >> 4);
         umma_f16_if(leader, d, a, k, id_s, c > 0);
 #pragma unroll
@@ -288,44 +306,49 @@ prefill_attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
         if (last) umma_commit_if(leader, &ctl->empty[at.st]);
       }
       umma_commit_if(leader, &ctl->s_full[t]);
-      return true;
     };
-    auto values = [&](int t, int j, bool last) {
-      if (!wait(&ctl->p_full[t], (uint32_t)j)) return false;
-      for (int c = 0; c < vc; ++c)
-        if (!wait(&ctl->full[vp.st + c], vp.turn)) return false;
-      tc_fence_after();
+    auto values = [&](int t, int j, bool first, bool last) {
+      until(&ctl->p_full[t], (uint32_t)j);
+      if (first)
+        for (int c = 0; c < vc; ++c) until(&ctl->full[vp.st + c], vp.turn);
       const uint64_t v = v_desc + (uint32_t)vp.st * (kPfChunk >> 4);
       const uint32_t d = tmem + 256 + t * 128, a = tmem + t * 128;
+      umma_f16_ts_if(leader, d, a, v, id_o, j > 0);
 #pragma unroll
-      for (int ks = 0; ks < kPfTile / 16; ++ks) umma_f16_ts_if(leader, d, a + ks * 8, v + ks * (2048 >> 4), id_o, ks > 0 || j > 0);
+      for (int ks = 1; ks < kPfTile / 16; ++ks) umma_f16_ts_if(leader, d, a + ks * 8, v + ks * (2048 >> 4), id_o, true);
       if (last)
         for (int c = 0; c < vc; ++c) umma_commit_if(leader, &ctl->empty[vp.st + c]);
       umma_commit_if(leader, &ctl->pv_done[t]);
-      return true;
     };
-    // The value tile behind the key tile at kp, then the next key tile.
-    auto to_values = [&]() {
-      vp = kp;
-      for (int c = 0; c < kc; ++c) vp.step(n_slots);
-      if (vc == 2 && vp.st == n_slots - 1) {
-        const bool r = wait(&ctl->full[vp.st], vp.turn);
-        umma_commit_if(leader, &ctl->empty[vp.st]);
-        vp.step(n_slots);
-        return r;
+    // One copy of each product's code for both tiles: what the issuing warp
+    // runs has to stay in the instruction cache beside the softmax.
+    const int n0 = n_t[0], n1 = n_t[1];
+    if (n_all > 0) until(&ctl->q_full, 0);
+#pragma unroll 1
+    for (int j = -1; j < n_all && ok; ++j) {
+      if (j >= 0) {
+        // the value tile lies behind the key tile at kp, the next key tile behind that
+        vp = kp;
+        for (int c = 0; c < kc; ++c) vp.step(n_slots);
+        if (vc == 2 && vp.st == n_slots - 1) {
+          until(&ctl->full[vp.st], vp.turn);
+          umma_commit_if(leader, &ctl->empty[vp.st]);
+          vp.step(n_slots);
+        }
+        kp = vp;
+        for (int c = 0; c < vc; ++c) kp.step(n_slots);
       }
-      return true;
-    };
-    if (ok && n_t[0] > 0) ok = scores(0, n_t[1] == 0);
-    if (ok && n_t[1] > 0) ok = scores(1, true);
-    for (int j = 0; j < n_all && ok; ++j) {
-      ok = to_values();
-      kp = vp;
-      for (int c = 0; c < vc; ++c) kp.step(n_slots);
-      if (ok && j < n_t[0]) ok = values(0, j, j >= n_t[1]);
-      if (ok && j + 1 < n_t[0]) ok = scores(0, j + 1 >= n_t[1]);
-      if (ok && j < n_t[1]) ok = values(1, j, true);
-      if (ok && j + 1 < n_t[1]) ok = scores(1, true);
+#pragma unroll 1
+      for (int t = 0; t < 2; ++t) {
+        const int mine = t ? n1 : n0, other = t ? n0 : n1;
+        // the first tile to use a slot waits for it, the last one releases it
+        if (j >= 0 && j < mine) values(t, j, t == 0 || j >= other, t == 1 || j >= other);
+        if (j + 1 < mine) scores(t, t == 0 || j + 1 >= other, t == 1 || j + 1 >= other);
+      }
+    }
+    if (!ok) {   // TMEM and shared memory go with the CTA: let the products in flight end
+      umma_commit_if(leader, &ctl->drained);
+      wait(&ctl->drained, 0);
     }
   } else {
     // ------------------------------------------------------------- softmax
@@ -335,24 +358,25 @@ prefill_attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
     const uint32_t s_at = tmem + lanes + t * 128, o_at = tmem + lanes + 256 + t * 128;
     const int64_t last64 = p.causal ? smin<int64_t>((int64_t)s.nk - s.nq + i, s.nk - 1) : s.nk - 1;
     const int last = (int)smax<int64_t>(last64, -1);     // the last key it sees
-    const float to2 = fabsf(p.scale) * 1.4426950408889634f;
-    const uint32_t flip = p.scale < 0.0f ? 0x80000000u : 0u;
+    // A scale that is not positive is applied to the logits beforehand.
+    const bool odd = !(p.scale > 0.0f);
+    const float to2 = p.scale == 0.0f ? 1.0f : fabsf(p.scale) * 1.4426950408889634f, first = p.scale == 0.0f ? 0.0f : -1.0f;
     float m = -CUDART_INF_F, l = 0.0f;
     bool ok = true;
     for (int j = 0; j < n_t[t]; ++j) {
       ok = wait(&ctl->s_full[t], (uint32_t)j);
       if (!ok) break;
       tc_fence_after();
-      // Twice over the row: the maximum from the upper half and the lower one,
-      // then the probabilities from the lower half, still in registers, and the
-      // upper one, loaded again (P overwrites only what has been read).  All 128
-      // at once would not fit the 168 registers a thread has.
+      // Twice over the row, 64 columns at a time in a loop: once for the
+      // maximum, once for the probabilities (P overwrites only what has been
+      // read).  Unrolled over all 128 columns the code falls out of the
+      // instruction cache, and the issuing warp waits for its own.
       const int left = last - j * kPfTile;   // columns up to this one are seen
       const bool cut = __any_sync(0xffffffffu, left < kPfTile - 1);
-      auto fix = [&](uint32_t (&x)[32], int c0) {   // sign of the scale, unseen columns
-        if (flip) {
+      auto fix = [&](uint32_t (&x)[32], int c0) {
+        if (odd) {
 #pragma unroll
-          for (int c = 0; c < 32; ++c) x[c] ^= 0x80000000u;
+          for (int c = 0; c < 32; ++c) x[c] = __float_as_uint(__uint_as_float(x[c]) * first);
         }
         if (cut) {
 #pragma unroll
@@ -360,29 +384,24 @@ prefill_attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
             if (c0 + c > left) x[c] = 0xff800000u;
         }
       };
-      float top[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
-      auto largest = [&](const uint32_t (&x)[32]) {
-#pragma unroll
-        for (int c = 0; c < 32; ++c) top[c & 3] = fmaxf(top[c & 3], __uint_as_float(x[c]));
-      };
       uint32_t v0[32], v1[32];
-      tmem_ld32(s_at + 64, v0);
-      tmem_ld32(s_at + 96, v1);
-      tmem_wait_ld();
-      fix(v0, 64);
-      fix(v1, 96);
-      largest(v0);
-      largest(v1);
+      float top[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
       tmem_ld32(s_at, v0);
-      tmem_ld32(s_at + 32, v1);
-      tmem_wait_ld();
-      fix(v0, 0);
-      fix(v1, 32);
-      largest(v0);
-      largest(v1);
+#pragma unroll 1
+      for (int c = 0; c < 128; c += 64) {
+        tmem_wait_ld();
+        tmem_ld32(s_at + c + 32, v1);
+        fix(v0, c);
+#pragma unroll
+        for (int k = 0; k < 32; ++k) top[k & 3] = fmaxf(top[k & 3], __uint_as_float(v0[k]));
+        tmem_wait_ld();
+        tmem_ld32(s_at + ((c + 64) & 127), v0);   // at the end the first columns, for the second time
+        fix(v1, c + 32);
+#pragma unroll
+        for (int k = 0; k < 32; ++k) top[k & 3] = fmaxf(top[k & 3], __uint_as_float(v1[k]));
+      }
       const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-      // -inf (nothing seen) stays so even at scale 0
-      const float y = most == -CUDART_INF_F ? most : most * to2;
+      const float y = most * to2;
       if (__any_sync(0xffffffffu, y > m + kPfLift)) {
         const float mn = fmaxf(m, y), f = mn == m ? 1.0f : exp2f(m - mn);
         m = mn;
@@ -391,45 +410,41 @@ prefill_attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
           ok = wait(&ctl->pv_done[t], (uint32_t)(j - 1));
           if (!ok) break;
           tc_fence_after();
+          tmem_wait_ld();
+#pragma unroll 1
           for (int c = 0; c < 64 * vc; c += 32) {
-            uint32_t w[32];
-            tmem_ld32(o_at + c, w);
+            tmem_ld32(o_at + c, v1);
             tmem_wait_ld();
 #pragma unroll
-            for (int k = 0; k < 32; ++k) w[k] = __float_as_uint(__uint_as_float(w[k]) * f);
-            tmem_st32(o_at + c, w);
+            for (int k = 0; k < 32; ++k) v1[k] = __float_as_uint(__uint_as_float(v1[k]) * f);
+            tmem_st32(o_at + c, v1);
           }
         }
       }
       const float ref = m == -CUDART_INF_F ? 0.0f : m;
       float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-      auto exps = [&](const uint32_t (&x)[32], int c) {   // P of columns 32 c ..
+      auto exps = [&](const uint32_t (&x)[32], int c) {   // P of columns c .. c + 31
         uint32_t w[16];
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
-          const uint32_t r0 = x[2 * k], r1 = x[2 * k + 1];
-          float a = fmaf(__uint_as_float(r0), to2, -ref), e = fmaf(__uint_as_float(r1), to2, -ref);
-          if (to2 == 0.0f) {   // 0 x -inf
-            a = r0 == 0xff800000u ? -CUDART_INF_F : a;
-            e = r1 == 0xff800000u ? -CUDART_INF_F : e;
-          }
-          a = ex2_approx(a);
-          e = ex2_approx(e);
+          const float a = ex2_approx(fmaf(__uint_as_float(x[2 * k]), to2, -ref));
+          const float e = ex2_approx(fmaf(__uint_as_float(x[2 * k + 1]), to2, -ref));
           sum[k & 3] += a + e;
           w[k] = pack_bf16(a, e);
         }
-        tmem_st16(s_at + 16 * c, w);
+        tmem_st16(s_at + c / 2, w);
       };
-      exps(v0, 0);
-      tmem_ld32(s_at + 64, v0);
-      exps(v1, 1);
-      tmem_wait_ld();
-      tmem_ld32(s_at + 96, v1);
-      fix(v0, 64);
-      exps(v0, 2);
-      tmem_wait_ld();
-      fix(v1, 96);
-      exps(v1, 3);
+#pragma unroll 1
+      for (int c = 0; c < 128; c += 64) {
+        tmem_wait_ld();
+        tmem_ld32(s_at + c + 32, v1);
+        fix(v0, c);
+        exps(v0, c);
+        tmem_wait_ld();
+        if (c == 0) tmem_ld32(s_at + 64, v0);
+        fix(v1, c + 32);
+        exps(v1, c + 32);
+      }
       l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
       tmem_wait_st();
       tc_fence_before();
