@@ -11,16 +11,16 @@
 // of the second product straight from TMEM, so shared memory holds queries,
 // keys and values only.
 //   warp 0     loads with TMA: the queries once, then K and V in 128 x 64
-//              chunks through a ring.  In key tiles that end behind the
-//              sequence it clears the rows of V behind the end, and in tiles on
-//              the diagonal it looks for infinities and NaN among values that
-//              some rows must not see (a probability of 0 would not hide them):
-//              if there are any, the rows are computed again one by one at the
-//              end;
+//              chunks through a ring;
 //   warp 1     issues tcgen05.mma;
 //   warps 2-9  softmax, a thread a query: the reference maximum moves only when
 //              a logit exceeds it by more than 2^8 (then the thread rescales its
 //              row of O), so no thread waits for another one.
+//   warps 10, 11  look after chunks of V that not every query may see whole: they
+//              clear the rows behind the end of the sequence, and infinities
+//              and NaN in rows on the diagonal (a probability of 0 would not
+//              hide them from the rows that must not see them); rows that do see
+//              one are computed again one by one at the end.
 // CTAs start with the queries that see most keys, all heads of them, so that
 // the short ones fill up the end.
 #pragma once
@@ -43,7 +43,7 @@ struct PrefillAttend {
 
 constexpr int kPfTile = 128;                     // queries a tile, keys a tile
 constexpr int kPfChunk = kPfTile * 128;          // bytes of 128 rows x 64 columns
-constexpr int kPfThreads = 320;
+constexpr int kPfThreads = 384;
 constexpr int kPfMaxSlots = 12;
 constexpr int kPfControlBytes = 1024;
 constexpr float kPfLift = 8.0f;
@@ -76,7 +76,8 @@ __host__ inline size_t pf_smem_bytes(int key_chunks) {
 
 struct PfControl {
   uint64_t full[kPfMaxSlots], empty[kPfMaxSlots];
-  uint64_t q_full, landed, drained;
+  uint64_t landed[kPfMaxSlots];   // a chunk of V that is looked after first
+  uint64_t q_full, drained;
   uint64_t s_full[2], p_full[2], pv_done[2];
   uint32_t tmem_base;
   int poison;   // first key whose values some rows must not see
@@ -191,9 +192,9 @@ prefill_attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
     for (int i = 0; i < n_slots; ++i) {
       mbar_init(&ctl->full[i], 1);
       mbar_init(&ctl->empty[i], 1);
+      mbar_init(&ctl->landed[i], 1);
     }
     mbar_init(&ctl->q_full, 1);
-    mbar_init(&ctl->landed, 1);
     mbar_init(&ctl->drained, 1);
     for (int t = 0; t < 2; ++t) {
       mbar_init(&ctl->s_full[t], 1);
@@ -212,12 +213,19 @@ prefill_attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
     return __shfl_sync(0xffffffffu, (int)mbar_wait_within(bar, parity & 1, limit, nullptr), 0) != 0;
   };
 
+  // Rows of V in key tile j that exist and that every query of the CTA sees.
+  auto live_rows = [&](int j) { return smin(s.nk - j * kPfTile, kPfTile); };
+  auto common_rows = [&](int j) {
+    const int64_t n = p.causal ? (int64_t)s.nk - s.nq + q0 + 1 - (int64_t)j * kPfTile : kPfTile;
+    return (int)smax<int64_t>(0, smin<int64_t>(n, kPfTile));
+  };
+  auto touched = [&](int j) { return __shfl_sync(0xffffffffu, (int)(smin(live_rows(j), common_rows(j)) < kPfTile), 0) != 0; };
+
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     const uint32_t leader = elect_one();
     bool ok = n_all > 0;
     PfRing slot;
-    uint32_t touched = 0;
     if (ok) {
       mbar_expect_if(leader, &ctl->q_full, (uint32_t)(2 * kc) * kPfChunk);
       for (int t = 0; t < 2; ++t)
@@ -242,38 +250,13 @@ prefill_attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
         if (ok && leader) mbar_arrive(&ctl->full[slot.st]);
         slot.step(n_slots);
       }
-      // Rows of V behind the end of the sequence; rows that not every query sees.
-      const int live = smin(s.nk - j * kPfTile, kPfTile);
-      const int64_t all_see = p.causal ? (int64_t)s.nk - s.nq + q0 + 1 - (int64_t)j * kPfTile : kPfTile;
-      const bool touch = live < kPfTile || all_see < live;
-      PfRing first = slot;
-      if (ok && touch) mbar_expect_if(leader, &ctl->landed, (uint32_t)vc * kPfChunk);
+      const bool touch = touched(j);
       for (int c = 0; c < vc && ok; ++c, slot.step(n_slots)) {
         if (slot.turn > 0) ok = wait(&ctl->empty[slot.st], slot.turn - 1);
         if (!ok) break;
-        if (!touch) mbar_expect_if(leader, &ctl->full[slot.st], kPfChunk);
-        tma_load_3d_if(leader, ring + slot.st * kPfChunk, &map_v, touch ? &ctl->landed : &ctl->full[slot.st], c * 64, g, row);
-      }
-      if (ok && touch) {
-        ok = wait(&ctl->landed, touched++);
-        if (!ok) break;
-        int bad = INT32_MAX;
-        const int from = (int)smax<int64_t>(all_see, 0);
-        for (int c = 0; c < vc; ++c) {
-          unsigned char *chunk = ring + (first.st + c) * kPfChunk;
-          for (int i = from * 8 + lane; i < live * 8; i += 32) {
-            uint4 *at = reinterpret_cast<uint4 *>(chunk + i * 16);
-            if (clear_not_finite<0x7f80u>(*at)) bad = smin(bad, j * kPfTile + (i >> 3));
-          }
-          for (int i = live * 8 + lane; i < kPfTile * 8; i += 32)
-            *reinterpret_cast<uint4 *>(chunk + i * 16) = make_uint4(0u, 0u, 0u, 0u);
-        }
-        if (bad != INT32_MAX) atomicMin(&ctl->poison, bad);
-        fence_async_smem();
-        __syncwarp();
-        if (leader)
-          for (int c = 0; c < vc; ++c) mbar_arrive(&ctl->full[first.st + c]);
-        __syncwarp();
+        uint64_t *bar = touch ? &ctl->landed[slot.st] : &ctl->full[slot.st];
+        mbar_expect_if(leader, bar, kPfChunk);
+        tma_load_3d_if(leader, ring + slot.st * kPfChunk, &map_v, bar, c * 64, g, row);
       }
     }
     if (!ok && n_all > 0) {   // let the copies in flight land before the CTA ends
@@ -350,6 +333,39 @@ prefill_attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
       umma_commit_if(leader, &ctl->drained);
       wait(&ctl->drained, 0);
     }
+  } else if (warp >= 10) {
+    // ------------------------------------------------ chunks of V seen in part
+    const int c = warp - 10;
+    PfRing slot;
+    uint32_t seen = 0;   // a slot's uses of this kind, modulo 2: the parity of its barrier
+    bool ok = c < vc;
+    for (int j = 0; j < n_all && ok; ++j) {
+      for (int k = 0; k < kc; ++k) slot.step(n_slots);
+      if (vc == 2 && slot.st == n_slots - 1) slot.step(n_slots);
+      if (touched(j)) {
+        const int at = slot.st + c;
+        ok = wait(&ctl->landed[at], seen >> at);
+        if (!ok) break;
+        seen ^= 1u << at;
+        int bad = INT32_MAX;
+        const int live = live_rows(j);
+        uint4 *chunk = reinterpret_cast<uint4 *>(ring + at * kPfChunk);
+#pragma unroll 8
+        for (int i = common_rows(j) * 8 + lane; i < live * 8; i += 32) {
+          uint4 v = chunk[i];
+          if (clear_not_finite<0x7f80u>(v)) {
+            chunk[i] = v;
+            bad = smin(bad, j * kPfTile + (i >> 3));
+          }
+        }
+        for (int i = live * 8 + lane; i < kPfTile * 8; i += 32) chunk[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (bad != INT32_MAX) atomicMin(&ctl->poison, bad);
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->full[at]);
+      }
+      for (int k = 0; k < vc; ++k) slot.step(n_slots);
+    }
   } else {
     // ------------------------------------------------------------- softmax
     const int t = (warp - 2) >> 2, quad = warp & 3;
@@ -393,12 +409,12 @@ prefill_attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
         tmem_ld32(s_at + c + 32, v1);
         fix(v0, c);
 #pragma unroll
-        for (int k = 0; k < 32; ++k) top[k & 3] = fmaxf(top[k & 3], __uint_as_float(v0[k]));
+        for (int k = 0; k < 32; k += 2) top[(k >> 1) & 3] = fmaxf(fmaxf(top[(k >> 1) & 3], __uint_as_float(v0[k])), __uint_as_float(v0[k + 1]));
         tmem_wait_ld();
         tmem_ld32(s_at + ((c + 64) & 127), v0);   // at the end the first columns, for the second time
         fix(v1, c + 32);
 #pragma unroll
-        for (int k = 0; k < 32; ++k) top[k & 3] = fmaxf(top[k & 3], __uint_as_float(v1[k]));
+        for (int k = 0; k < 32; k += 2) top[(k >> 1) & 3] = fmaxf(fmaxf(top[(k >> 1) & 3], __uint_as_float(v1[k])), __uint_as_float(v1[k + 1]));
       }
       const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
       const float y = most * to2;
@@ -422,14 +438,17 @@ prefill_attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
         }
       }
       const float ref = m == -CUDART_INF_F ? 0.0f : m;
-      float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      uint64_t sum[4] = {0u, 0u, 0u, 0u};   // pairs of fp32
+      const uint64_t to2_2 = pair_f32(to2, to2), ref_2 = pair_f32(-ref, -ref);
       auto exps = [&](const uint32_t (&x)[32], int c) {   // P of columns c .. c + 31
         uint32_t w[16];
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
-          const float a = ex2_approx(fmaf(__uint_as_float(x[2 * k]), to2, -ref));
-          const float e = ex2_approx(fmaf(__uint_as_float(x[2 * k + 1]), to2, -ref));
-          sum[k & 3] += a + e;
+          float a, e;
+          unpair_f32(fma_f32x2(pair_f32(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), to2_2, ref_2), a, e);
+          a = ex2_approx(a);
+          e = ex2_approx(e);
+          sum[k & 3] = add_f32x2(sum[k & 3], pair_f32(a, e));
           w[k] = pack_bf16(a, e);
         }
         tmem_st16(s_at + c / 2, w);
@@ -445,7 +464,11 @@ prefill_attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
         fix(v1, c + 32);
         exps(v1, c + 32);
       }
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      {
+        float a, e;
+        unpair_f32(add_f32x2(add_f32x2(sum[0], sum[1]), add_f32x2(sum[2], sum[3])), a, e);
+        l += a + e;
+      }
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
