@@ -245,6 +245,27 @@ __device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
   return (uint32_t)__half_as_ushort(__low2half(h)) | ((uint32_t)__half_as_ushort(__high2half(h)) << 16);
 }
 
+// Eight 4-bit codes (even columns in the low bits of their bytes) times a
+// scale given twice: four pairs of fp16.
+__device__ __forceinline__ void codes_to_half(uint32_t codes, uint32_t scale2, uint32_t (&o)[4]) {
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t.reg .b32 h0, h1, h2, h3;\n\t"
+      "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 h0, b0;\n\tcvt.rn.f16x2.e2m1x2 h1, b1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 h2, b2;\n\tcvt.rn.f16x2.e2m1x2 h3, b3;\n\t"
+      "mul.rn.f16x2 %0, h0, %5;\n\tmul.rn.f16x2 %1, h1, %5;\n\t"
+      "mul.rn.f16x2 %2, h2, %5;\n\tmul.rn.f16x2 %3, h3, %5;\n\t}"
+      : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3])
+      : "r"(codes), "r"(scale2));
+}
+// Two e4m3 scales, each as a pair of equal fp16.
+__device__ __forceinline__ void scales_to_half(unsigned short two, uint32_t (&o)[2]) {
+  asm("{\n\t.reg .b32 h;\n\t.reg .b16 a, b;\n\t"
+      "cvt.rn.f16x2.e4m3x2 h, %2;\n\tmov.b32 {a, b}, h;\n\t"
+      "mov.b32 %0, {a, a};\n\tmov.b32 %1, {b, b};\n\t}"
+      : "=r"(o[0]), "=r"(o[1])
+      : "h"(two));
+}
+
 template <int NB, bool FP4>
 __global__ void __launch_bounds__(la_threads(FP4), 1)
 latent_attend_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant__ CUtensorMap map_q,
@@ -827,18 +848,13 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_co
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             unsigned char *line = ring + sl * kLaSlot + (c >> 1) * (kLaTile * 128) + tok * 128;
-            const __half2 both = __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two[c], __NV_E4M3));
-            const __half2 sc[2] = {__half2half2(__low2half(both)), __half2half2(__high2half(both))};
+            uint32_t sc[2];
+            scales_to_half(two[c], sc);
             const uint32_t w[4] = {code[c].x, code[c].y, code[c].z, code[c].w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               uint32_t o[4];
-#pragma unroll
-              for (int b = 0; b < 4; ++b) {
-                const __half2 h = __hmul2(
-                    __half2(__nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)(w[i] >> (8 * b)), __NV_E2M1)), sc[i >> 1]);
-                o[b] = (uint32_t)__half_as_ushort(__low2half(h)) | ((uint32_t)__half_as_ushort(__high2half(h)) << 16);
-              }
+              codes_to_half(w[i], sc[i >> 1], o);
               *reinterpret_cast<uint4 *>(line + ((((c & 1) * 4 + i) ^ (tok & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
             }
           }
