@@ -40,7 +40,7 @@ s4r_status latent_attend_shape(const s4r_latent_attend_args *a) {
     return S4R_ERR_INVALID_ARG;
   if (a->rank % 8 || a->rank > S4R_MAX_LATENT_RANK || a->batch > S4R_MAX_REQUESTS ||
       (int64_t)a->n_query * a->n_heads > INT32_MAX / S4R_MAX_LATENT_WIDTH ||
-      (int64_t)a->n_query * a->n_heads * a->batch > INT32_MAX ||
+      (int64_t)a->n_query * a->n_heads * a->batch > INT32_MAX || (int64_t)a->n_query * a->n_heads > 65536 ||
       (int64_t)a->max_pages * a->page_size > INT32_MAX)
     return S4R_ERR_UNSUPPORTED;
   return S4R_OK;
@@ -48,7 +48,7 @@ s4r_status latent_attend_shape(const s4r_latent_attend_args *a) {
 
 // Blocks of query rows, grid and workspace of a latent attention call.
 struct LatentPlan {
-  int nb, row_blocks, n_ctas;
+  int nb, row_blocks, n_groups;   // the grid: row_blocks CTAs for each of n_groups ranges of tiles
   size_t unit_poison, part_poison, units, ml, part, total;
 };
 LatentPlan latent_plan(const s4r_latent_attend_args *a) {
@@ -56,19 +56,20 @@ LatentPlan latent_plan(const s4r_latent_attend_args *a) {
   const int64_t rows = (int64_t)a->n_query * a->n_heads;
   l.row_blocks = (int)ceil_div(rows, 64);
   l.nb = la_block_rows(rows);
-  const int64_t tiles = (int64_t)a->batch * l.row_blocks * ceil_div((int64_t)a->max_pages * a->page_size, kLaTile);
-  l.n_ctas = (int)smax<int64_t>(1, smin<int64_t>(tiles, sm_count()));
+  const int64_t tiles = (int64_t)a->batch * ceil_div((int64_t)a->max_pages * a->page_size, kLaTile);
+  l.n_groups = (int)smax<int64_t>(1, smin<int64_t>(tiles, sm_count() / l.row_blocks));
+  const size_t n_ctas = (size_t)l.n_groups * l.row_blocks;
   size_t off = kAlign;   // status word
   l.unit_poison = off;
   off += round_up(sizeof(int32_t) * (size_t)a->batch * l.row_blocks);
   l.part_poison = off;
-  off += round_up(sizeof(int32_t) * 2 * (size_t)l.n_ctas);
+  off += round_up(sizeof(int32_t) * 2 * n_ctas);
   l.units = off;
   off += round_up(sizeof(int2) * (size_t)a->batch * l.row_blocks);
   l.ml = off;
-  off += round_up(sizeof(float2) * 2 * (size_t)l.n_ctas * l.nb);
+  off += round_up(sizeof(float2) * 2 * n_ctas * l.nb);
   l.part = off;
-  off += round_up(sizeof(float) * 2 * (size_t)l.n_ctas * l.nb * a->rank);
+  off += round_up(sizeof(float) * 2 * n_ctas * l.nb * a->rank);
   l.total = off;
   return l;
 }
@@ -108,7 +109,7 @@ s4r_status latent_attend_launch(const LatentAttend &p, cudaStream_t st) {
   const size_t smem = (size_t)la_layout(NB, p.width, FP4).total;
   cudaError_t err = ensure_smem<latent_attend_kernel<NB, FP4>>(smem);
   if (err != cudaSuccess) return fail("latent_attend_kernel (shared memory)", err);
-  latent_attend_kernel<NB, FP4><<<(unsigned)p.n_ctas, la_threads(FP4), smem, st>>>(kv, q, p);
+  latent_attend_kernel<NB, FP4><<<(unsigned)(p.n_groups * p.row_blocks), la_threads(FP4), smem, st>>>(kv, q, p);
   if (check_launch("latent_attend_kernel") != S4R_OK) return S4R_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   // Few rows with many parts each: their columns go to CTAs of their own.
@@ -258,7 +259,7 @@ s4r_status s4r_latent_attend(const s4r_latent_attend_args *a, void *stream) {
   p.lse = a->lse;
   p.rows = a->n_query * a->n_heads;
   p.row_blocks = l.row_blocks;
-  p.n_ctas = l.n_ctas;
+  p.n_groups = l.n_groups;
   p.slots = la_layout(l.nb, a->width, fp4).slots;
   p.status = reinterpret_cast<uint32_t *>(ws);
   p.unit_poison = reinterpret_cast<int32_t *>(ws + l.unit_poison);

@@ -9,10 +9,12 @@
 // to HBM alone.
 //
 // latent_attend_kernel: a persistent grid, one CTA per SM.  The work is the
-// stream of 64-token tiles of all (request, block of NB query rows) units, cut
-// into equal consecutive ranges, so ragged batches and single long requests
-// load every SM alike; a unit that crosses a border leaves partial sums, which
-// latent_combine_kernel joins (no CTA waits for another one).
+// stream of 64-token tiles of all requests, cut into equal consecutive ranges,
+// so ragged batches and single long requests load every SM alike; a request
+// that crosses a border leaves partial sums, which latent_combine_kernel joins
+// (no CTA waits for another one).  With more than NB query rows a request, a
+// range belongs to as many CTAs as there are blocks of NB rows: they read the
+// same tiles at the same time, so L2 serves all but one.
 //
 // Both products are computed transposed, tokens on M: S^T = K Q^T (M = 64
 // tokens, N = NB) and O^T = V^T P^T (M = 128 latent columns, N = NB).  So few
@@ -72,15 +74,15 @@ struct LatentAttend {
   bf16 *out;
   float *lse;
   // plan
-  int32_t rows, row_blocks, n_ctas, slots;   // query rows a request, blocks of NB of them, grid, ring slots
+  int32_t rows, row_blocks, n_groups, slots; // query rows a request, blocks of NB of them, ranges of tiles, ring slots
   // workspace
   uint32_t *status;
   // first row with a value that some query rows must not see (see latent_combine_kernel), INT32_MAX for none: of a
   // unit that one CTA computes whole, of a part
-  int32_t *unit_poison, *part_poison;        // [batch * row_blocks], [2 * n_ctas]
+  int32_t *unit_poison, *part_poison;        // [batch * row_blocks], [2 * CTAs]
   int2 *units;                               // [batch * row_blocks] first part, and how many (1: computed whole)
-  float2 *ml;                                // [2 * n_ctas][NB] reference maximum and sum of a partial
-  float *part;                               // [2 * n_ctas][NB][rank] unscaled partial results
+  float2 *ml;                                // [2 * CTAs][NB] reference maximum and sum of a partial
+  float *part;                               // [2 * CTAs][NB][rank] unscaled partial results
 };
 
 // Query rows a block of the kernel takes, and how many blocks a request has.
@@ -138,8 +140,8 @@ __device__ __forceinline__ int32_t la_length(const LatentAttend &p, int b) {
 }
 __device__ __forceinline__ int32_t la_tiles(int32_t len) { return (len + kLaTile - 1) / kLaTile; }
 
-// Tiles a CTA takes of `total`.
-__host__ __device__ inline long long la_share(long long total, int n_ctas) { return (total + n_ctas - 1) / n_ctas; }
+// Tiles of a range, of `total`.
+__host__ __device__ inline long long la_share(long long total, int n_groups) { return (total + n_groups - 1) / n_groups; }
 
 // A place in a ring of n slots and the parity of its turn (no divisions: the
 // single-warp roles are bound by the instructions they issue).
@@ -154,9 +156,9 @@ struct LaRing {
   }
 };
 
-// The segments of a CTA: consecutive tiles of one unit.
+// The segments of a CTA: consecutive tiles of one request.
 struct LaSegment {
-  int b, rb, tile, n, unit_tiles, len, index;
+  int b, tile, n, unit_tiles, len, index;
 };
 struct LaWalk {
   int b, off, left, index;
@@ -167,13 +169,12 @@ struct LaWalk {
     while (true) {   // requests without rows have no tiles
       len = la_length(p, b);
       nt = la_tiles(len);
-      if (off < nt * p.row_blocks) break;
+      if (off < nt) break;
       off = 0;
       ++b;
     }
     s.b = b;
-    s.rb = off / nt;
-    s.tile = off - s.rb * nt;
+    s.tile = off;
     s.n = smin(nt - s.tile, left);
     s.unit_tiles = nt;
     s.len = len;
@@ -246,7 +247,9 @@ __device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
 }
 
 // Eight 4-bit codes (even columns in the low bits of their bytes) times a
-// scale given twice: four pairs of fp16.
+// scale given twice: four pairs of fp16.  (Putting the codes' bits in fp16's
+// place with shifts and byte permutes took 6% more time for the whole kernel
+// than the conversion instruction.)
 __device__ __forceinline__ void codes_to_half(uint32_t codes, uint32_t scale2, uint32_t (&o)[4]) {
   asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t.reg .b32 h0, h1, h2, h3;\n\t"
       "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
@@ -277,7 +280,7 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_co
   LaControl *ctl = reinterpret_cast<LaControl *>(smem + ly.control);
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int chunks = (p.width + 63) / 64, pairs = (chunks + 1) / 2, vblocks = (p.rank + 127) / 128;
-  const int n_slots = p.slots;
+  const int n_slots = p.slots, rb = blockIdx.x % p.row_blocks;   // this CTA's block of query rows
   const long long limit = wait_limit();
   constexpr int kStatCols = 4 * NB;   // S^T behind the four blocks of O^T
 
@@ -313,7 +316,7 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_co
     for (int b = b0; b < b1; ++b) {
       const int32_t n = p.lengths[b];
       if (blockIdx.x == 0 && (n < 0 || n > (int64_t)p.max_pages * p.page_size)) set_status(p.status, kDevStatusCheck);
-      mine += (long long)la_tiles(la_length(p, b)) * p.row_blocks;
+      mine += la_tiles(la_length(p, b));
     }
     long long before = mine, total = 0;   // inclusive over the warp first
 #pragma unroll
@@ -329,12 +332,12 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_co
       if (w < warp) before += v;
       total += v;
     }
-    const long long share = la_share(total, p.n_ctas), start = share * blockIdx.x;
+    const long long share = la_share(total, p.n_groups), start = share * (blockIdx.x / p.row_blocks);
     if (start < total && start >= before && start < before + mine) {
       long long at = before;
       int b = b0;
       while (true) {
-        const long long n = (long long)la_tiles(la_length(p, b)) * p.row_blocks;
+        const long long n = la_tiles(la_length(p, b));
         if (start < at + n) break;
         at += n;
         ++b;
@@ -368,7 +371,6 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_co
     };
     while (ok && __shfl_sync(0xffffffffu, (int)walk.next(p, s), 0)) {
       s.b = __shfl_sync(0xffffffffu, s.b, 0);
-      s.rb = __shfl_sync(0xffffffffu, s.rb, 0);
       s.tile = __shfl_sync(0xffffffffu, s.tile, 0);
       s.n = __shfl_sync(0xffffffffu, s.n, 0);
       s.len = __shfl_sync(0xffffffffu, s.len, 0);
@@ -394,7 +396,7 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_co
         if (!ok) break;
         mbar_expect_if(leader, &ctl->q_full, (uint32_t)(chunks * NB * 128));
         for (int c = 0; c < chunks; ++c)
-          tma_load_2d_if(leader, smem + ly.q + c * NB * 128, &map_q, &ctl->q_full, c * 64, s.b * p.rows + s.rb * NB);
+          tma_load_2d_if(leader, smem + ly.q + c * NB * 128, &map_q, &ctl->q_full, c * 64, s.b * p.rows + rb * NB);
       }
       for (int j = s.tile; j < s.tile + s.n && ok; ++j) {
         if (left == 0) {   // 32 is a multiple of a tile's boxes
@@ -602,7 +604,7 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_co
 #pragma unroll
           for (int i = 0; i < R; ++i) {
             int sees = all_see;
-            if (p.n_query > 1) sees += smin(s.rb * NB + r0 + 8 * (i >> 1) + 2 * (lane & 3) + (i & 1), p.rows - 1) / p.n_heads;
+            if (p.n_query > 1) sees += smin(rb * NB + r0 + 8 * (i >> 1) + 2 * (lane & 3) + (i & 1), p.rows - 1) / p.n_heads;
             if (tok >= sees) y0[i] = -CUDART_INF_F;
             if (tok + 8 >= sees) y1[i] = -CUDART_INF_F;
           }
@@ -707,39 +709,42 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_co
         if (lane == 0) mbar_arrive(&ctl->p_full);
       }
       if (!ok) break;
-      // End of the segment: sums over the tokens, then the result.
+      // End of the segment: sums over the tokens (a thread a row), then the
+      // result.
       la_bar(bar);   // wmax is free
 #pragma unroll
       for (int i = 0; i < R; ++i) {
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], o);
-        if (lane < 4) ctl->wmax[quad][r0 + 8 * (i >> 1) + 2 * lane + (i & 1)] = l[i];
+        const int row = r0 + 8 * (i >> 1) + 2 * (lane & 3) + (i & 1);
+        if (lane < 4) {
+          ctl->wmax[quad][row] = l[i];
+          if (quad == 0) ctl->fac[row] = m[i];
+        }
       }
       const bool whole = s.n == s.unit_tiles;
       const int part = 2 * (int)blockIdx.x + (s.index > 0 ? 1 : 0);
-      const int rows = smin(NB, p.rows - s.rb * NB);
-      const int64_t row0 = (int64_t)s.b * p.rows + s.rb * NB;
+      const int rows = smin(NB, p.rows - rb * NB);
+      const int64_t row0 = (int64_t)s.b * p.rows + rb * NB;
       la_bar(bar);
-      if (quad == 0 && lane < 4) {
-#pragma unroll
-        for (int i = 0; i < R; ++i) {
-          const int row = r0 + 8 * (i >> 1) + 2 * lane + (i & 1);
-          const float sum = (ctl->wmax[0][row] + ctl->wmax[1][row]) + (ctl->wmax[2][row] + ctl->wmax[3][row]);
-          if (whole) {
-            ctl->fac[row] = sum > 0.0f || sum != sum ? (FP4 ? p.cache_scale : 1.0f) / sum : 0.0f;
-            if (p.lse && row < rows)
-              p.lse[row0 + row] = m[i] == -CUDART_INF_F && !(sum != sum) ? -CUDART_INF_F : (m[i] + log2f(sum)) * 0.6931471805599453f;
-          } else if (row < rows) {
-            p.ml[(int64_t)part * NB + row] = make_float2(m[i], sum);
-          }
+      if (tid < NB / 2) {
+        const int row = r0 + tid;
+        const float sum = (ctl->wmax[0][row] + ctl->wmax[1][row]) + (ctl->wmax[2][row] + ctl->wmax[3][row]);
+        const float top = ctl->fac[row];
+        if (whole) {
+          ctl->fac[row] = sum > 0.0f || sum != sum ? (FP4 ? p.cache_scale : 1.0f) / sum : 0.0f;
+          if (p.lse && row < rows)
+            p.lse[row0 + row] = top == -CUDART_INF_F && !(sum != sum) ? -CUDART_INF_F : (top + log2f(sum)) * 0.6931471805599453f;
+        } else if (row < rows) {
+          p.ml[(int64_t)part * NB + row] = make_float2(top, sum);
         }
       }
       // The CTA with a unit's first tile says which parts there will be: its
-      // own one (the second if it began with another unit) and the first one
-      // of each CTA behind it.
+      // own one (the second if it began with another request) and the first
+      // one of each CTA behind it that has the same query rows.
       if (s.tile == 0 && tid == 0 && grp == 0) {
         const int rest = s.unit_tiles - s.n, share = ctl->share;
-        p.units[s.b * p.row_blocks + s.rb] = make_int2(part, 1 + (rest + share - 1) / share);
+        p.units[s.b * p.row_blocks + rb] = make_int2(part, 1 + (rest + share - 1) / share);
       }
       if (p.n_query > 1) {
         // each group has looked at one half of the columns
@@ -748,34 +753,58 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_co
         la_bar_all();
         if (tid == 0 && grp == 0) {
           for (int w = 1; w < kLaSoftmaxWarps; ++w) poison = smin(poison, ctl->poison[w]);
-          (whole ? p.unit_poison[s.b * p.row_blocks + s.rb] : p.part_poison[part]) = poison;
+          (whole ? p.unit_poison[s.b * p.row_blocks + rb] : p.part_poison[part]) = poison;
         }
       }
       la_bar(bar);
       if (!mbar_wait_within(&ctl->pv_done, (n - 1) & 1, limit, p.status)) ctl->fail = 1;
       __syncwarp();
       tc_fence_after();
-      for (int vb = 0; vb < vblocks; ++vb) {
-        const int col = vb * 128 + quad * 32 + lane;
-        bf16 *out = p.out + (row0 + r0) * p.rank + col;
-        float *pt = p.part + ((int64_t)part * NB + r0) * p.rank + col;
-        for (int c = r0; c < r0 + NB / 2 && c < rows; c += 8) {
-          uint32_t w[8];
+      if (whole) {
+        float f[NB / 2];   // of this group's rows
+#pragma unroll
+        for (int i = 0; i < NB / 2; ++i) f[i] = ctl->fac[r0 + i];
+        const bool up1 = lane & 1, up2 = lane & 2, up4 = lane & 4;
+        bf16 *out = p.out + (row0 + r0 + (lane & 7)) * p.rank + quad * 32 + (lane & 24);
+        for (int vb = 0; vb < vblocks; ++vb, out += 128) {
+          uint32_t w[NB / 16][8];
           __syncwarp();
-          tmem_ld8(tmem + lanes + vb * NB + c, w);
+#pragma unroll
+          for (int c = 0; c < NB / 16; ++c) tmem_ld8(tmem + lanes + vb * NB + r0 + 8 * c, w[c]);
           tmem_wait_ld();
-          const int live = col < p.rank ? rows - c : 0;
-          if (whole) {
+          const bool in = vb * 128 + quad * 32 + (lane & 24) < p.rank;
 #pragma unroll
-            for (int i = 0; i < 8; ++i, out += p.rank) {
-              const float f = ctl->fac[c + i];
-              if (i < live) *out = from_f<bf16>(f == 0.0f ? 0.0f : __uint_as_float(w[i]) * f);
+          for (int c = 0; c < NB / 16; ++c) {
+            // Eight columns of one row a lane, by exchanges with the lanes 1, 2
+            // and 4 away: a 16-byte store.
+            uint32_t q[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t t = pack_bf16(__uint_as_float(w[c][2 * i]) * f[8 * c + 2 * i],
+                                           __uint_as_float(w[c][2 * i + 1]) * f[8 * c + 2 * i + 1]);
+              const uint32_t x = __shfl_xor_sync(0xffffffffu, t, 1);
+              q[i] = up1 ? __byte_perm(x, t, 0x7632) : __byte_perm(t, x, 0x5410);   // row 2 i + lane % 2
             }
-          } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i, pt += p.rank)
-              if (i < live) *pt = __uint_as_float(w[i]);
+            const uint32_t xa = __shfl_xor_sync(0xffffffffu, up2 ? q[0] : q[1], 2), xb = __shfl_xor_sync(0xffffffffu, up2 ? q[2] : q[3], 2);
+            const uint32_t a0 = up2 ? xa : q[0], a1 = up2 ? q[1] : xa, b0 = up2 ? xb : q[2], b1 = up2 ? q[3] : xb;
+            const uint32_t x0 = __shfl_xor_sync(0xffffffffu, up4 ? a0 : b0, 4), x1 = __shfl_xor_sync(0xffffffffu, up4 ? a1 : b1, 4);
+            if (in && r0 + 8 * c + (lane & 7) < rows)
+              *reinterpret_cast<uint4 *>(out + (int64_t)8 * c * p.rank) = up4 ? make_uint4(x0, x1, b0, b1) : make_uint4(a0, a1, x0, x1);
           }
+        }
+      } else {
+        float *pt = p.part + ((int64_t)part * NB + r0) * p.rank + quad * 32 + lane;
+        for (int vb = 0; vb < vblocks; ++vb, pt += 128) {
+          uint32_t w[NB / 16][8];
+          __syncwarp();
+#pragma unroll
+          for (int c = 0; c < NB / 16; ++c) tmem_ld8(tmem + lanes + vb * NB + r0 + 8 * c, w[c]);
+          tmem_wait_ld();
+          const int live = vb * 128 + quad * 32 + lane < p.rank ? rows - r0 : 0;
+          float *at = pt;
+#pragma unroll
+          for (int i = 0; i < NB / 2; ++i, at += p.rank)
+            if (i < live) *at = __uint_as_float(w[i / 8][i % 8]);
         }
       }
       tc_fence_before();
@@ -795,8 +824,8 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_co
       // queries: one warp a row, scaled so that the largest value lies in [2^14, 2^15)
       if (s.index > 0 && !mbar_wait_within(&ctl->q_empty, (uint32_t)(s.index - 1) & 1, limit, p.status)) break;
       for (int row = dw; row < NB; row += kLaDequantWarps) {
-        const bool live = s.rb * NB + row < p.rows;
-        const bf16 *src = p.q + ((int64_t)s.b * p.rows + s.rb * NB + row) * p.width;
+        const bool live = rb * NB + row < p.rows;
+        const bf16 *src = p.q + ((int64_t)s.b * p.rows + rb * NB + row) * p.width;
         float x[2 * ((S4R_MAX_LATENT_WIDTH + 63) / 64)];
         float top = 0.0f;
 #pragma unroll
@@ -909,7 +938,7 @@ __global__ void __launch_bounds__(kLcThreads) latent_combine_kernel(const Latent
   if (p.n_query > 1) {
     if (parts.y <= 1) poison = p.unit_poison[unit];
     else
-      for (int i = 0; i < parts.y; ++i) poison = smin(poison, p.part_poison[i == 0 ? parts.x : 2 * (parts.x / 2 + i)]);
+      for (int i = 0; i < parts.y; ++i) poison = smin(poison, p.part_poison[i == 0 ? parts.x : 2 * (parts.x / 2 + i * p.row_blocks)]);
   }
   if (sees > poison) {
     if (blockIdx.y > 0) return;
@@ -953,10 +982,10 @@ __global__ void __launch_bounds__(kLcThreads) latent_combine_kernel(const Latent
   }
   if (parts.y <= 1) return;
   // Part 0 lies in slot parts.x, the others in the first slot of the CTAs
-  // behind it.  Statistics first, a thread a part; then the warps share out the
+  // behind it, row_blocks CTAs apart.  Statistics first, a thread a part; then the warps share out the
   // parts, a lane adding up 4 neighbouring columns of every 128.
   const int r = row - rb * NB;
-  auto slot_of = [&](int i) { return (int64_t)(i == 0 ? parts.x : 2 * (parts.x / 2 + i)) * NB + r; };
+  auto slot_of = [&](int i) { return (int64_t)(i == 0 ? parts.x : 2 * (parts.x / 2 + i * p.row_blocks)) * NB + r; };
   float top = -CUDART_INF_F;
   for (int i = threadIdx.x; i < parts.y; i += kLcThreads) top = fmaxf(top, p.ml[slot_of(i)].x);
   top = warp_max(top);
@@ -985,21 +1014,25 @@ __global__ void __launch_bounds__(kLcThreads) latent_combine_kernel(const Latent
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < W; ++w) sum += sl[w];
-#pragma unroll 4
-    for (int i = warp; i < m; i += W) {
+    auto add = [&](int i, int k) {
       const float w = f_s[i];
-      const float *src = p.part + slot_of(base + i) * p.rank;
-#pragma unroll
-      for (int k = 0; k < S4R_MAX_LATENT_RANK / 128; ++k) {
-        const int col = col0 + 128 * k;
-        if (col < col1 && w != 0.0f) {   // a part of weight 0 may hold infinities
-          const float4 x = *reinterpret_cast<const float4 *>(src + col);
-          o[k].x = fmaf(w, x.x, o[k].x);
-          o[k].y = fmaf(w, x.y, o[k].y);
-          o[k].z = fmaf(w, x.z, o[k].z);
-          o[k].w = fmaf(w, x.w, o[k].w);
-        }
+      const int col = col0 + 128 * k;
+      if (col < col1 && w != 0.0f) {   // a part of weight 0 may hold infinities
+        const float4 x = *reinterpret_cast<const float4 *>(p.part + slot_of(base + i) * p.rank + col);
+        o[k].x = fmaf(w, x.x, o[k].x);
+        o[k].y = fmaf(w, x.y, o[k].y);
+        o[k].z = fmaf(w, x.z, o[k].z);
+        o[k].w = fmaf(w, x.w, o[k].w);
       }
+    };
+    if (cols == 128) {   // many parts, few columns: more loads under way
+#pragma unroll 16
+      for (int i = warp; i < m; i += W) add(i, 0);
+    } else {
+#pragma unroll 2
+      for (int i = warp; i < m; i += W)
+#pragma unroll
+        for (int k = 0; k < S4R_MAX_LATENT_RANK / 128; ++k) add(i, k);
     }
   }
 #pragma unroll
