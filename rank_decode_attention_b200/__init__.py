@@ -333,48 +333,71 @@ def s4r_reconstruct(coeffs: torch.Tensor, basis: torch.Tensor, rows: torch.Tenso
 _BF16, _F32, _I32, _I64, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.int64, torch.uint8
 
 
-def _arg(what: str, name: str, t, dtype, shape, dense_from: int = 0):
-    """Check that tensor `t` has the type, the shape (None: any extent), the current device and unit-stride rows: its
-    dimensions from `dense_from` on are contiguous.  Returns its data pointer."""
+def _device() -> int:
+    """Index of the current CUDA device; -2 (no tensor's) without one."""
+    try:
+        return torch.cuda.current_device()
+    except (RuntimeError, AssertionError):
+        return -2
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_on(stream, dev: int):
+    """Handle of `stream`, or of the current stream of device `dev` (a serving loop makes these calls every step: the
+    current stream without a Stream object around it)."""
+    if stream is None and _raw_stream is not None and dev >= 0:
+        return _raw_stream(dev)
+    return _stream(stream)
+
+
+def _arg(what: str, name: str, t, dtype, shape, dev: int, dense_from: int = 0):
+    """Data pointer of tensor `t`, which must have the type, the shape, the device `dev` and contiguous dimensions from
+    `dense_from` on."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
     if t.dtype is not dtype:
         raise ValueError(f"{what}: {name} must be {dtype}, got {t.dtype}")
-    dims = t.shape
-    if len(dims) != len(shape):
-        raise ValueError(f"{what}: {name} must have {len(shape)} dimensions, got {tuple(dims)}")
-    for d, n in zip(dims, shape):
-        if n is not None and d != n:
-            raise ValueError(f"{what}: {name} must have shape {tuple(shape)}, got {tuple(dims)}")
-    if not t.is_contiguous():
-        step = 1
-        strides = t.stride()
-        for i in range(len(dims) - 1, dense_from - 1, -1):
-            if dims[i] != 1 and strides[i] != step:
-                raise ValueError(f"{what}: {name} must be contiguous" + (f" from dimension {dense_from} on" if dense_from else ""))
-            step *= dims[i]
-        if dense_from == 0:
-            raise ValueError(f"{what}: {name} must be contiguous")
-    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+    if t.shape != shape:
+        raise ValueError(f"{what}: {name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    step = 1
+    for i in range(len(shape) - 1, dense_from - 1, -1):
+        if shape[i] != 1 and t.stride(i) != step:
+            raise ValueError(f"{what}: {name} must be contiguous" + (f" from dimension {dense_from} on" if dense_from else ""))
+        step *= shape[i]
+    if t.get_device() != dev:
         raise ValueError(f"{what}: {name} must be on the current CUDA device, got {t.device}")
     return t.data_ptr()
 
 
-def _workspace(what: str, t):
+def _dims(what: str, name: str, t, n: int):
+    """Shape of a tensor of `n` dimensions."""
+    s = t.shape
+    if len(s) != n:
+        raise ValueError(f"{what}: {name} must have {n} dimensions, got {tuple(s)}")
+    return s
+
+
+def _workspace(what: str, t, dev: int):
     """(pointer, bytes) of a workspace tensor or (None, 0)."""
     if t is None:
         return None, 0
-    if not t.is_cuda or t.get_device() != torch.cuda.current_device() or not t.is_contiguous():
+    if t.get_device() != dev or not t.is_contiguous():
         raise ValueError(f"{what}: the workspace must be contiguous and on the current CUDA device, got {t.device}")
     return t.data_ptr(), t.numel() * t.element_size()
 
 
-def _latent_cache(what: str, cache, width: int, page_size: int):
+def _latent_cache(what: str, cache, width: int, page_size: int, dev: int):
     """(S4R type, pages, pointer) of a paged cache: bf16 [pages][page_size][width], or uint8
     [pages][page_size * width * 9 // 16] (4-bit)."""
     if cache.dtype is _U8:
         if page_size * width % 16:
             raise ValueError(f"{what}: a 4-bit page holds whole groups of 16 columns")
-        return S4R_FP4, cache.shape[0], _arg(what, "cache", cache, _U8, (None, page_size * width * 9 // 16))
-    return S4R_BF16, cache.shape[0], _arg(what, "cache", cache, _BF16, (None, page_size, width))
+        n = _dims(what, "cache", cache, 2)[0]
+        return S4R_FP4, n, _arg(what, "cache", cache, _U8, (n, page_size * width * 9 // 16), dev)
+    n = _dims(what, "cache", cache, 3)[0]
+    return S4R_BF16, n, _arg(what, "cache", cache, _BF16, (n, page_size, width), dev)
 
 
 def s4r_page_plan(*, lengths, new_tokens, block_table, free_pages, free_count, lengths_out, free_count_out, cu_tokens,
@@ -382,48 +405,52 @@ def s4r_page_plan(*, lengths, new_tokens, block_table, free_pages, free_count, l
     """Block tables and slot maps of a step on the device (see include/s4r.h): lengths, new_tokens, lengths_out [B],
     block_table [B][max_pages], free_pages [capacity], free_count, free_count_out [1], cu_tokens [B+1] int32; slots
     [max_tokens] int64, positions and requests [max_tokens] int32 or None."""
-    w = "s4r_page_plan"
-    B, n = lengths.shape[0], slots.shape[0]
+    w, dev = "s4r_page_plan", _device()
+    B, n, one = lengths.shape[0], slots.shape[0], (1,)
+    cols, capacity = _dims(w, "block_table", block_table, 2)[1], free_pages.shape[0]
+    per, per_token = (B,), (n,)
     a = PagePlanArgs(
-        B, page_size, block_table.shape[-1], free_pages.shape[0], n,
-        _arg(w, "lengths", lengths, _I32, (B,)), _arg(w, "new_tokens", new_tokens, _I32, (B,)),
-        _arg(w, "block_table", block_table, _I32, (B, None)), _arg(w, "free_pages", free_pages, _I32, (None,)),
-        _arg(w, "free_count", free_count, _I32, (1,)), _arg(w, "lengths_out", lengths_out, _I32, (B,)),
-        _arg(w, "free_count_out", free_count_out, _I32, (1,)), _arg(w, "cu_tokens", cu_tokens, _I32, (B + 1,)),
-        _arg(w, "slots", slots, _I64, (n,)),
-        None if positions is None else _arg(w, "positions", positions, _I32, (n,)),
-        None if requests is None else _arg(w, "requests", requests, _I32, (n,)),
-        _workspace(w, status_workspace)[0])
-    return _check(lib().s4r_page_plan(ctypes.byref(a), _stream(stream)), w)
+        B, page_size, cols, capacity, n,
+        _arg(w, "lengths", lengths, _I32, per, dev), _arg(w, "new_tokens", new_tokens, _I32, per, dev),
+        _arg(w, "block_table", block_table, _I32, (B, cols), dev), _arg(w, "free_pages", free_pages, _I32, (capacity,), dev),
+        _arg(w, "free_count", free_count, _I32, one, dev), _arg(w, "lengths_out", lengths_out, _I32, per, dev),
+        _arg(w, "free_count_out", free_count_out, _I32, one, dev), _arg(w, "cu_tokens", cu_tokens, _I32, (B + 1,), dev),
+        _arg(w, "slots", slots, _I64, per_token, dev),
+        None if positions is None else _arg(w, "positions", positions, _I32, per_token, dev),
+        None if requests is None else _arg(w, "requests", requests, _I32, per_token, dev),
+        None if status_workspace is None else _workspace(w, status_workspace, dev)[0])
+    return _check(lib().s4r_page_plan(ctypes.byref(a), _stream_on(stream, dev)), w)
 
 
 def s4r_latent_write(*, latents, slots, cache, page_size, cache_scale=1.0, stored=None, status_workspace=None,
                      stream=None) -> int:
     """Store latents [n][width] bf16 (row stride may exceed width) at slots [n] int64 of a paged cache: bf16
     [pages][page_size][width] or uint8 [pages][page_size*width*9//16] (4-bit, see include/s4r.h)."""
-    w = "s4r_latent_write"
-    n, width = latents.shape
-    dt, pages, cache_ptr = _latent_cache(w, cache, width, page_size)
+    w, dev = "s4r_latent_write", _device()
+    n, width = _dims(w, "latents", latents, 2)
+    dt, pages, cache_ptr = _latent_cache(w, cache, width, page_size, dev)
     a = LatentWriteArgs(
-        n, width, page_size, pages, dt, cache_scale, _arg(w, "latents", latents, _BF16, (n, width), 1),
-        latents.stride(0) if n > 1 else width, _arg(w, "slots", slots, _I64, (n,)), cache_ptr,
-        None if stored is None else _arg(w, "stored", stored, _BF16, (n, width)), _workspace(w, status_workspace)[0])
-    return _check(lib().s4r_latent_write(ctypes.byref(a), _stream(stream)), w)
+        n, width, page_size, pages, dt, cache_scale, _arg(w, "latents", latents, _BF16, (n, width), dev, 1),
+        latents.stride(0) if n > 1 else width, _arg(w, "slots", slots, _I64, (n,), dev), cache_ptr,
+        None if stored is None else _arg(w, "stored", stored, _BF16, (n, width), dev),
+        None if status_workspace is None else _workspace(w, status_workspace, dev)[0])
+    return _check(lib().s4r_latent_write(ctypes.byref(a), _stream_on(stream, dev)), w)
 
 
 def latent_attend_args(*, q, cache, block_table, lengths, out, page_size, scale, lse=None, cache_scale=1.0,
                        workspace=None) -> LatentAttendArgs:
     """Fill s4r_latent_attend_args: q [B][n_query][H][width] bf16, cache as in s4r_latent_write, block_table
     [B][max_pages] and lengths [B] int32, out [B][n_query][H][rank] bf16, lse [B][n_query][H] float32 or None."""
-    w = "s4r_latent_attend"
-    B, T, H, width = q.shape
-    dt, pages, cache_ptr = _latent_cache(w, cache, width, page_size)
-    ws, ws_bytes = _workspace(w, workspace)
+    w, dev = "s4r_latent_attend", _device()
+    B, T, H, width = _dims(w, "q", q, 4)
+    rank, cols = _dims(w, "out", out, 4)[3], _dims(w, "block_table", block_table, 2)[1]
+    dt, pages, cache_ptr = _latent_cache(w, cache, width, page_size, dev)
+    ws, ws_bytes = _workspace(w, workspace, dev)
     return LatentAttendArgs(
-        B, T, H, width, out.shape[-1], page_size, block_table.shape[-1], dt, pages, scale, cache_scale,
-        _arg(w, "q", q, _BF16, (B, T, H, width)), cache_ptr, _arg(w, "block_table", block_table, _I32, (B, None)),
-        _arg(w, "lengths", lengths, _I32, (B,)), _arg(w, "out", out, _BF16, (B, T, H, None)),
-        None if lse is None else _arg(w, "lse", lse, _F32, (B, T, H)), ws, ws_bytes)
+        B, T, H, width, rank, page_size, cols, dt, pages, scale, cache_scale,
+        _arg(w, "q", q, _BF16, (B, T, H, width), dev), cache_ptr, _arg(w, "block_table", block_table, _I32, (B, cols), dev),
+        _arg(w, "lengths", lengths, _I32, (B,), dev), _arg(w, "out", out, _BF16, (B, T, H, rank), dev),
+        None if lse is None else _arg(w, "lse", lse, _F32, (B, T, H), dev), ws, ws_bytes)
 
 
 def s4r_latent_attend_workspace_bytes(args: LatentAttendArgs) -> int:
@@ -432,25 +459,25 @@ def s4r_latent_attend_workspace_bytes(args: LatentAttendArgs) -> int:
 
 def s4r_latent_attend(args: LatentAttendArgs, stream=None) -> int:
     """Attention over a paged latent cache, absorbed form (see include/s4r.h)."""
-    return _check(lib().s4r_latent_attend(ctypes.byref(args), _stream(stream)), "s4r_latent_attend")
+    return _check(lib().s4r_latent_attend(ctypes.byref(args), _stream_on(stream, _device())), "s4r_latent_attend")
 
 
 def s4r_latent_project(x, basis, out, *, to_latent: bool, stream=None) -> int:
     """Per-head products with basis [H*head_dim][rank] bf16: x [n][H][head_dim] to out [n][H][rank] (to_latent), or x
     [n][H][rank] (or [n][rank], one row for all heads) to out [n][H][head_dim].  Token and head strides are free."""
-    w = "s4r_latent_project"
-    n, H, n_out = out.shape
+    w, dev = "s4r_latent_project", _device()
+    n, H, n_out = _dims(w, "out", out, 3)
     n_in = x.shape[-1]
     dim, rank = (n_in, n_out) if to_latent else (n_out, n_in)
     shared = x.dim() == 2
-    xp = _arg(w, "x", x, _BF16, (n, n_in) if shared else (n, H, n_in), 1 if shared else 2)
-    op = _arg(w, "out", out, _BF16, (n, H, n_out), 2)
+    xp = _arg(w, "x", x, _BF16, (n, n_in) if shared else (n, H, n_in), dev, 1 if shared else 2)
+    op = _arg(w, "out", out, _BF16, (n, H, n_out), dev, 2)
     a = LatentProjectArgs(
         n, H, dim, rank, 1 if to_latent else 0, xp, x.stride(0) if n > 1 else H * n_in,
         0 if shared else (x.stride(1) if H > 1 else n_in),
-        _arg(w, "basis", basis, _BF16, (H * dim, rank)), op, out.stride(0) if n > 1 else H * n_out,
+        _arg(w, "basis", basis, _BF16, (H * dim, rank), dev), op, out.stride(0) if n > 1 else H * n_out,
         out.stride(1) if H > 1 else n_out)
-    return _check(lib().s4r_latent_project(ctypes.byref(a), _stream(stream)), w)
+    return _check(lib().s4r_latent_project(ctypes.byref(a), _stream_on(stream, dev)), w)
 
 
 def prefill_attend_args(*, q, k, v, cu_q, cu_k, max_q, scale, out, k_rope=None, lse=None,
@@ -458,26 +485,26 @@ def prefill_attend_args(*, q, k, v, cu_q, cu_k, max_q, scale, out, k_rope=None, 
     """Fill s4r_prefill_attend_args: q [total_q][Hq][head_dim + rope_dim], k [total_k][Hkv][head_dim], v
     [total_k][Hkv][value_dim], k_rope [total_k][rope_dim] or None, out [total_q][Hq][value_dim] bf16 (token strides of k,
     v, k_rope are free), cu_q and cu_k [B+1] int32, lse [total_q][Hq] float32 or None."""
-    w = "s4r_prefill_attend"
-    nq, Hq, dq = q.shape
-    nk, Hkv, dim = k.shape
-    vd = v.shape[-1]
-    rope = 0 if k_rope is None else k_rope.shape[-1]
+    w, dev = "s4r_prefill_attend", _device()
+    nq, Hq, _ = _dims(w, "q", q, 3)
+    nk, Hkv, dim = _dims(w, "k", k, 3)
+    vd = _dims(w, "v", v, 3)[2]
+    rope = 0 if k_rope is None else _dims(w, "k_rope", k_rope, 2)[1]
     B = cu_q.shape[0] - 1
     return PrefillAttendArgs(
         B, Hq, Hkv, dim, rope, vd, 1 if causal else 0, max_q, nq, nk, scale,
-        _arg(w, "q", q, _BF16, (nq, Hq, dim + rope)), _arg(w, "k", k, _BF16, (nk, Hkv, dim), 1),
-        _arg(w, "v", v, _BF16, (nk, Hkv, vd), 1),
-        None if k_rope is None else _arg(w, "k_rope", k_rope, _BF16, (nk, rope), 1),
+        _arg(w, "q", q, _BF16, (nq, Hq, dim + rope), dev), _arg(w, "k", k, _BF16, (nk, Hkv, dim), dev, 1),
+        _arg(w, "v", v, _BF16, (nk, Hkv, vd), dev, 1),
+        None if k_rope is None else _arg(w, "k_rope", k_rope, _BF16, (nk, rope), dev, 1),
         k.stride(0) if nk > 1 else Hkv * dim, v.stride(0) if nk > 1 else Hkv * vd,
         0 if k_rope is None else (k_rope.stride(0) if nk > 1 else rope),
-        _arg(w, "cu_q", cu_q, _I32, (B + 1,)), _arg(w, "cu_k", cu_k, _I32, (B + 1,)),
-        _arg(w, "out", out, _BF16, (nq, Hq, vd)), None if lse is None else _arg(w, "lse", lse, _F32, (nq, Hq)))
+        _arg(w, "cu_q", cu_q, _I32, (B + 1,), dev), _arg(w, "cu_k", cu_k, _I32, (B + 1,), dev),
+        _arg(w, "out", out, _BF16, (nq, Hq, vd), dev), None if lse is None else _arg(w, "lse", lse, _F32, (nq, Hq), dev))
 
 
 def s4r_prefill_attend(args: PrefillAttendArgs, stream=None) -> int:
     """Attention of ragged prompts over expanded keys and values (see include/s4r.h)."""
-    return _check(lib().s4r_prefill_attend(ctypes.byref(args), _stream(stream)), "s4r_prefill_attend")
+    return _check(lib().s4r_prefill_attend(ctypes.byref(args), _stream_on(stream, _device())), "s4r_prefill_attend")
 
 
 def s4r_read_device_status(workspace, stream=None) -> int:

@@ -196,7 +196,18 @@ s4r_status s4r_page_plan(const s4r_page_plan_args *a, void *stream) {
     return fail("page_plan_kernel (shared memory)", cudaGetLastError());
   const unsigned grid = grid_of(ceil_div(a->max_tokens, kPlanTokensPerCta), sm_count());
   page_plan_kernel<<<grid, kPlanThreads, smem, st>>>(p);
-  if (grid > 1) page_commit_kernel<<<1, kPlanThreads, smem, st>>>(p);
+  if (grid > 1) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(1);
+    cfg.blockDim = dim3(kPlanThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1] = {pdl_attr()};
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t err = cudaLaunchKernelEx(&cfg, page_commit_kernel, p);
+    if (err != cudaSuccess) return fail("page_commit_kernel", err);
+  }
   return check_launch("page_plan_kernel");
 }
 
@@ -216,10 +227,10 @@ s4r_status s4r_latent_write(const s4r_latent_write_args *a, void *stream) {
                 a->cache_scale, static_cast<const bf16 *>(a->latents), a->slots, static_cast<unsigned char *>(a->cache),
                 static_cast<bf16 *>(a->stored), static_cast<uint32_t *>(a->status_workspace)};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const int64_t items = a->n_tokens * (a->width / (a->cache_dtype == S4R_FP4 ? 16 : 8));
-  const unsigned grid = grid_of(ceil_div(items, 256), 16 * sm_count());
-  if (a->cache_dtype == S4R_FP4) latent_write_fp4<<<grid, 256, 0, st>>>(p);
-  else latent_write_bf16<<<grid, 256, 0, st>>>(p);
+  const unsigned grid = (unsigned)ceil_div(a->n_tokens, kWriteTokens);
+  if (a->cache_dtype == S4R_BF16) latent_write_bf16<<<grid, kWriteThreads, 0, st>>>(p);
+  else if (a->cache_scale == 1.0f) latent_write_fp4<true><<<grid, kWriteThreads, 0, st>>>(p);
+  else latent_write_fp4<false><<<grid, kWriteThreads, 0, st>>>(p);
   return check_launch("latent_write");
 }
 

@@ -4,6 +4,7 @@
 #pragma once
 #include <cuda_fp4.h>
 #include <cuda_fp8.h>
+#include <math_constants.h>
 
 #include "common.cuh"
 
@@ -147,6 +148,7 @@ __device__ inline void plan_commit(const PagePlan &p, const int32_t *s_pg, int32
 __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PagePlan p) {
   extern __shared__ int32_t plan_smem[];
   int32_t *s_tok = plan_smem, *s_pg = plan_smem + p.batch + 1;
+  if (gridDim.x > 1) pdl_trigger();   // the commit kernel may take its sums; it waits for this grid before it writes
   plan_scan(p, s_tok, s_pg);
   const int32_t total = s_tok[p.batch];
   const int32_t free_pages = plan_free(p, blockIdx.x == 0);
@@ -199,6 +201,7 @@ __global__ void __launch_bounds__(kPlanThreads) page_commit_kernel(const PagePla
   const int32_t free_pages = plan_free(p, false);
   const int32_t taken = s_pg[plan_find(s_pg, p.batch, free_pages)];
   __syncthreads();
+  pdl_wait();
   plan_commit(p, s_pg, free_pages, taken);
 }
 
@@ -220,14 +223,18 @@ __host__ __device__ inline int64_t latent_page_bytes(bool fp4, int32_t page_size
   return fp4 ? (int64_t)page_size * width * 9 / 16 : (int64_t)page_size * width * 2;
 }
 
+// A CTA takes kWriteTokens rows; within them every thread a piece at a time,
+// found with a 32-bit division.
+constexpr int kWriteTokens = 8, kWriteThreads = 256;
+
 // One thread a 16-byte piece of a row.
-__global__ void __launch_bounds__(256) latent_write_bf16(const LatentWrite p) {
-  const int32_t per = p.width / 8;
-  const int64_t n = p.n_tokens * per;
-  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x) {
-    const int64_t t = i / per;
-    const int32_t c = (int32_t)(i - t * per);
-    const int64_t slot = p.slots[t];
+__global__ void __launch_bounds__(kWriteThreads) latent_write_bf16(const LatentWrite p) {
+  const uint32_t per = (uint32_t)p.width / 8;
+  const int64_t t0 = (int64_t)blockIdx.x * kWriteTokens;
+  const uint32_t n = (uint32_t)smin<int64_t>(kWriteTokens, p.n_tokens - t0) * per;
+  for (uint32_t i = threadIdx.x; i < n; i += kWriteThreads) {
+    const uint32_t r = i / per, c = i - r * per;
+    const int64_t t = t0 + r, slot = p.slots[t];
     if (slot < 0) continue;
     if (slot >= p.n_rows) {
       if (c == 0) set_status(p.status, kDevStatusCheck);
@@ -239,16 +246,22 @@ __global__ void __launch_bounds__(256) latent_write_bf16(const LatentWrite p) {
 }
 
 // One thread a group of 16 columns: 32 bytes in, 8 bytes of codes and one
-// scale byte out.  Quotients are IEEE divisions, so that the codes follow from
-// the definition bit by bit.
-__global__ void __launch_bounds__(256) latent_write_fp4(const LatentWrite p) {
-  const int32_t per = p.width / 16;
-  const int64_t n = p.n_tokens * per;
+// scale byte out.  The codes follow from the definition bit by bit.  ONE
+// (cache_scale 1): the quotients need no division.  x has 8 significant bits
+// and the scale 4, so x / scale is either exactly a border between two codes
+// (at most 3 bits) or a part in 2^15 away from every border; the product with
+// the rounded reciprocal is within 2^-22 of it, and rounded to 20 bits it is on
+// the border, or on the same side of it, as the quotient is.  (With divisions
+// the 32765 rows of 576 columns took 21.4 us, 16 x 9 instructions a group.)
+template <bool ONE>
+__global__ void __launch_bounds__(kWriteThreads) latent_write_fp4(const LatentWrite p) {
+  const uint32_t per = (uint32_t)p.width / 16;
+  const int64_t t0 = (int64_t)blockIdx.x * kWriteTokens;
+  const uint32_t n = (uint32_t)smin<int64_t>(kWriteTokens, p.n_tokens - t0) * per;
   const int64_t page_bytes = latent_page_bytes(true, p.page_size, p.width);
-  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x) {
-    const int64_t t = i / per;
-    const int32_t g = (int32_t)(i - t * per);
-    const int64_t slot = p.slots[t];
+  for (uint32_t i = threadIdx.x; i < n; i += kWriteThreads) {
+    const uint32_t r = i / per, g = i - r * per;
+    const int64_t t = t0 + r, slot = p.slots[t];
     const bool bad = slot >= p.n_rows;
     if (bad && g == 0) set_status(p.status, kDevStatusCheck);
     if ((slot < 0 || bad) && !p.stored) continue;
@@ -258,17 +271,24 @@ __global__ void __launch_bounds__(256) latent_write_fp4(const LatentWrite p) {
     float top = 0.0f;
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
-      if (p.cache_scale != 1.0f) x[j] = __fdiv_rn(x[j], p.cache_scale);
+      if (!ONE) x[j] = __fdiv_rn(x[j], p.cache_scale);
       top = fmaxf(top, fabsf(x[j]));
     }
     const __nv_fp8_storage_t s8 = __nv_cvt_float_to_fp8(fminf(__fdiv_rn(top, 6.0f), 448.0f), __NV_SATFINITE, __NV_E4M3);
     const float s = __half2float(__half(__nv_cvt_fp8_to_halfraw(s8, __NV_E4M3)));
     uint32_t code[2] = {0u, 0u};
     if (s > 0.0f) {
+      const float inv = __frcp_rn(s);
+      auto quotient = [&](float v) {
+        if (!ONE) return __fdiv_rn(v, s);
+        const float q = v * inv;
+        // infinities and NaN have no bits to round
+        return fabsf(q) < CUDART_INF_F ? __uint_as_float((__float_as_uint(q) + 8u) & ~15u) : q;
+      };
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const __nv_fp4x2_storage_t c = __nv_cvt_float2_to_fp4x2(
-            make_float2(__fdiv_rn(x[2 * j], s), __fdiv_rn(x[2 * j + 1], s)), __NV_E2M1, cudaRoundNearest);
+        const __nv_fp4x2_storage_t c =
+            __nv_cvt_float2_to_fp4x2(make_float2(quotient(x[2 * j]), quotient(x[2 * j + 1])), __NV_E2M1, cudaRoundNearest);
         code[j >> 2] |= (uint32_t)c << (8 * (j & 3));
       }
     }
@@ -285,7 +305,8 @@ __global__ void __launch_bounds__(256) latent_write_fp4(const LatentWrite p) {
       for (int j = 0; j < 8; ++j) {
         const __half2 h = __half2(__nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)(code[j >> 2] >> (8 * (j & 3))), __NV_E2M1));
         const float2 f = __half22float2(h);
-        const __nv_bfloat162 b = __floats2bfloat162_rn(f.x * s * p.cache_scale, f.y * s * p.cache_scale);
+        const float m = ONE ? 1.0f : p.cache_scale;
+        const __nv_bfloat162 b = __floats2bfloat162_rn(f.x * s * m, f.y * s * m);
         w[j] = (uint32_t)__bfloat16_as_ushort(b.x) | ((uint32_t)__bfloat16_as_ushort(b.y) << 16);
       }
       uint4 *dst = reinterpret_cast<uint4 *>(p.stored + t * p.width + g * 16);
