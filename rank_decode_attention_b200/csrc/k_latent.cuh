@@ -48,6 +48,8 @@
 #include <cuda_fp8.h>
 #include <math_constants.h>
 
+#include <type_traits>
+
 #include "k_page.cuh"
 #include "umma.cuh"
 
@@ -1014,26 +1016,38 @@ __global__ void __launch_bounds__(kLcThreads) latent_combine_kernel(const Latent
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < W; ++w) sum += sl[w];
-    auto add = [&](int i, int k) {
-      const float w = f_s[i];
-      const int col = col0 + 128 * k;
-      if (col < col1 && w != 0.0f) {   // a part of weight 0 may hold infinities
-        const float4 x = *reinterpret_cast<const float4 *>(p.part + slot_of(base + i) * p.rank + col);
-        o[k].x = fmaf(w, x.x, o[k].x);
-        o[k].y = fmaf(w, x.y, o[k].y);
-        o[k].z = fmaf(w, x.z, o[k].z);
-        o[k].w = fmaf(w, x.w, o[k].w);
+    // Eight loads under way at a time, without a condition between them: of
+    // eight parts where there are many parts and few columns, else of two
+    // parts with up to four columns each.
+    auto batch = [&](int i0, auto parts_, auto ks_) {
+      constexpr int N = decltype(parts_)::value, K = decltype(ks_)::value;
+      float4 x[N][K];
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        const float *src = p.part + slot_of(base + smin(i0 + n * W, m - 1)) * p.rank;
+#pragma unroll
+        for (int k = 0; k < K; ++k) x[n][k] = *reinterpret_cast<const float4 *>(src + smin(col0 + 128 * k, p.rank - 4));
+      }
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        const float w = i0 + n * W < m ? f_s[i0 + n * W] : 0.0f;
+        if (w != 0.0f) {   // a part of weight 0 may hold infinities
+#pragma unroll
+          for (int k = 0; k < K; ++k) {
+            o[k].x = fmaf(w, x[n][k].x, o[k].x);
+            o[k].y = fmaf(w, x[n][k].y, o[k].y);
+            o[k].z = fmaf(w, x[n][k].z, o[k].z);
+            o[k].w = fmaf(w, x[n][k].w, o[k].w);
+          }
+        }
       }
     };
-    if (cols == 128) {   // many parts, few columns: more loads under way
-#pragma unroll 16
-      for (int i = warp; i < m; i += W) add(i, 0);
-    } else {
-#pragma unroll 2
-      for (int i = warp; i < m; i += W)
-#pragma unroll
-        for (int k = 0; k < S4R_MAX_LATENT_RANK / 128; ++k) add(i, k);
-    }
+    using std::integral_constant;
+    if (cols == 128)
+      for (int i = warp; i < m; i += 8 * W) batch(i, integral_constant<int, 8>{}, integral_constant<int, 1>{});
+    else
+      for (int i = warp; i < m; i += 2 * W)
+        batch(i, integral_constant<int, 2>{}, integral_constant<int, S4R_MAX_LATENT_RANK / 128>{});
   }
 #pragma unroll
   for (int k = 0; k < S4R_MAX_LATENT_RANK / 128; ++k)
