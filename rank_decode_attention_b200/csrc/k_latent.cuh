@@ -122,7 +122,7 @@ struct LaControl {
   uint64_t full[kLaMaxSlots], empty[kLaMaxSlots];
   uint64_t raw_full[kLaRawStages], raw_empty[kLaRawStages];
   uint64_t s_full[2], p_full, pv_done;
-  uint64_t q_full, q_empty, o_free;
+  uint64_t q_full, q_empty, o_free, drained;
   uint32_t tmem_base;
   int fail;   // a wait of the softmax warps gave up
   int first_b, first_off, n_tiles;   // start of this CTA's range and its length
@@ -300,6 +300,7 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_co
     mbar_init(&ctl->pv_done, 1);
     mbar_init(&ctl->q_full, FP4 ? kLaDequantWarps : 1);
     mbar_init(&ctl->q_empty, 1);
+    mbar_init(&ctl->drained, 1);
     mbar_init(&ctl->o_free, kLaSoftmaxWarps);
     mbar_fence_init();
     ctl->fail = 0;
@@ -541,7 +542,12 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_co
         ++n;
       }
     }
-    if (ok && due) second();
+    if (ok && due) ok = second();
+    if (!ok) {   // TMEM and shared memory go with the CTA: let the products in flight end
+      umma_commit_if(leader, &ctl->drained);
+      mbar_wait_within(&ctl->drained, 0, kWaitCycles, p.status);
+      __syncwarp();
+    }
   } else if (warp < 2 + kLaSoftmaxWarps) {
     // ------------------------------------------------------------- softmax
     // Two groups of four warps, each with half of the query rows and all tokens;

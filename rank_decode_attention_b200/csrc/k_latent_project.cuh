@@ -48,7 +48,8 @@ latent_project_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_co
   unsigned char *staging = smem + kLpRing;
   uint64_t *full = reinterpret_cast<uint64_t *>(staging + kLpStage);
   uint64_t *empty = full + C::kStages, *acc_full = empty + C::kStages, *acc_empty = acc_full + 2;
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(acc_empty + 2);
+  uint64_t *drained = acc_empty + 2;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drained + 1);
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const long long limit = wait_limit();
   const int nk = (p.n_in + 63) / 64;
@@ -64,6 +65,7 @@ latent_project_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_co
       mbar_init(&acc_full[i], 1);
       mbar_init(&acc_empty[i], 4);
     }
+    mbar_init(drained, 1);
     mbar_fence_init();
     tma_prefetch_desc(&map_x);
     tma_prefetch_desc(&map_b);
@@ -159,6 +161,11 @@ latent_project_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_co
         }
       }
       if (ok) umma_commit_if(leader, &acc_full[acc]);
+    }
+    if (!ok) {   // TMEM and shared memory go with the CTA: let the products in flight end
+      umma_commit_if(leader, drained);
+      mbar_wait_within(drained, 0, kWaitCycles, nullptr);
+      __syncwarp();
     }
   } else {
     const int quad = warp & 3;

@@ -331,7 +331,8 @@ prefill_attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
     }
     if (!ok) {   // TMEM and shared memory go with the CTA: let the products in flight end
       umma_commit_if(leader, &ctl->drained);
-      wait(&ctl->drained, 0);
+      mbar_wait_within(&ctl->drained, 0, kWaitCycles, nullptr);
+      __syncwarp();
     }
   } else if (warp >= 10) {
     // ------------------------------------------------ chunks of V seen in part
