@@ -61,9 +61,9 @@ LatentPlan latent_plan(const s4r_latent_attend_args *a) {
   const size_t n_ctas = (size_t)l.n_groups * l.row_blocks;
   size_t off = kAlign;   // status word
   l.unit_poison = off;
-  off += round_up(sizeof(int32_t) * (size_t)a->batch * l.row_blocks);
+  off += round_up(sizeof(int2) * (size_t)a->batch * l.row_blocks);
   l.part_poison = off;
-  off += round_up(sizeof(int32_t) * 2 * n_ctas);
+  off += round_up(sizeof(int2) * 2 * n_ctas);
   l.units = off;
   off += round_up(sizeof(int2) * (size_t)a->batch * l.row_blocks);
   l.ml = off;
@@ -273,8 +273,8 @@ s4r_status s4r_latent_attend(const s4r_latent_attend_args *a, void *stream) {
   p.n_groups = l.n_groups;
   p.slots = la_layout(l.nb, a->width, fp4).slots;
   p.status = reinterpret_cast<uint32_t *>(ws);
-  p.unit_poison = reinterpret_cast<int32_t *>(ws + l.unit_poison);
-  p.part_poison = reinterpret_cast<int32_t *>(ws + l.part_poison);
+  p.unit_poison = reinterpret_cast<int2 *>(ws + l.unit_poison);
+  p.part_poison = reinterpret_cast<int2 *>(ws + l.part_poison);
   p.units = reinterpret_cast<int2 *>(ws + l.units);
   p.ml = reinterpret_cast<float2 *>(ws + l.ml);
   p.part = reinterpret_cast<float *>(ws + l.part);

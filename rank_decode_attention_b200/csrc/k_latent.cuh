@@ -79,9 +79,9 @@ struct LatentAttend {
   int32_t rows, row_blocks, n_groups, slots; // query rows a request, blocks of NB of them, ranges of tiles, ring slots
   // workspace
   uint32_t *status;
-  // first row with a value that some query rows must not see (see latent_combine_kernel), INT32_MAX for none: of a
-  // unit that one CTA computes whole, of a part
-  int32_t *unit_poison, *part_poison;        // [batch * row_blocks], [2 * CTAs]
+  // first row with a value that some query rows must not see (see latent_combine_kernel), INT32_MAX for none, as each
+  // softmax group found it: of a unit that one CTA computes whole, of a part
+  int2 *unit_poison, *part_poison;           // [batch * row_blocks], [2 * CTAs]
   int2 *units;                               // [batch * row_blocks] first part, and how many (1: computed whole)
   float2 *ml;                                // [2 * CTAs][NB] reference maximum and sum of a partial
   float *part;                               // [2 * CTAs][NB][rank] unscaled partial results
@@ -124,7 +124,6 @@ struct LaControl {
   uint64_t s_full[2], p_full, pv_done;
   uint64_t q_full, q_empty, o_free, drained;
   uint32_t tmem_base;
-  int fail;   // a wait of the softmax warps gave up
   int first_b, first_off, n_tiles;   // start of this CTA's range and its length
   int share;                         // tiles of a full range
   int poison[kLaSoftmaxWarps];
@@ -226,10 +225,6 @@ __device__ __forceinline__ void la_bar(int id) {
   __syncwarp();
   asm volatile("barrier.cta.sync.aligned %0, 128;" ::"r"(id) : "memory");
 }
-__device__ __forceinline__ void la_bar_all() {   // both groups
-  __syncwarp();
-  asm volatile("barrier.cta.sync.aligned 3, %0;" ::"n"(kLaSoftmaxWarps * 32) : "memory");
-}
 __device__ __forceinline__ bool la_bar_any(int id, bool x) {
   uint32_t r;
   __syncwarp();
@@ -303,7 +298,6 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_co
     mbar_init(&ctl->drained, 1);
     mbar_init(&ctl->o_free, kLaSoftmaxWarps);
     mbar_fence_init();
-    ctl->fail = 0;
     ctl->first_b = 0;
     ctl->first_off = 0;
     ctl->n_tiles = 0;
@@ -563,7 +557,7 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_co
         if (p.lse)
           for (int i = tid; i < p.rows; i += 128) p.lse[(int64_t)b * p.rows + i] = -CUDART_INF_F;
         for (int i = tid; i < p.row_blocks; i += 128) {
-          p.unit_poison[b * p.row_blocks + i] = INT32_MAX;
+          p.unit_poison[b * p.row_blocks + i] = make_int2(INT32_MAX, INT32_MAX);
           p.units[b * p.row_blocks + i] = make_int2(0, 1);
         }
       }
@@ -571,7 +565,7 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_co
     LaSegment s;
     uint32_t n = 0;
     LaRing slot;
-    bool ok = true;
+    bool ok = true, bad = false;   // bad: a wait of this thread gave up
     constexpr int R = NB / 8;   // query rows a thread sees: r0 + 8 (i / 2) + 2 (lane % 4) + i % 2
     while (ok && walk.next(p, s)) {
       float m[R], l[R], mul[R];
@@ -585,7 +579,7 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_co
       int poison = INT32_MAX;
       for (int j = s.tile; j < s.tile + s.n; ++j, ++n) {
         const uint32_t buf = n & 1;
-        if (!mbar_wait_within(&ctl->s_full[buf], (n >> 1) & 1, limit, p.status)) ctl->fail = 1;
+        if (!mbar_wait_within(&ctl->s_full[buf], (n >> 1) & 1, limit, p.status)) bad = true;
         __syncwarp();
         tc_fence_after();
         uint32_t v[2 * R];
@@ -593,7 +587,7 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_co
         tmem_wait_ld();
         if constexpr (FP4) {
           if (j == s.tile) {
-            if (!mbar_wait_within(&ctl->q_full, (uint32_t)s.index & 1, limit, p.status)) ctl->fail = 1;
+            if (!mbar_wait_within(&ctl->q_full, (uint32_t)s.index & 1, limit, p.status)) bad = true;
 #pragma unroll
             for (int i = 0; i < R; ++i)
               mul[i] = to2 * exp2f((float)-ctl->qexp[s.index & 1][r0 + 8 * (i >> 1) + 2 * (lane & 3) + (i & 1)]);
@@ -619,8 +613,10 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_co
         }
 #pragma unroll
         for (int i = 0; i < R; ++i) over |= fmaxf(y0[i], y1[i]) > m[i] + kLaLift;
-        over = la_bar_any(bar, over);
-        if (ctl->fail) {
+        // A wait that gave up in one thread ends the group as a whole: the second
+        // vote tells it from a moved maximum, so that all threads agree.
+        over = la_bar_any(bar, over || bad);
+        if (over && la_bar_any(bar, bad)) {
           ok = false;
           break;
         }
@@ -633,7 +629,7 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_co
           LaRing at = slot;
           for (int k = 0; k < pairs; ++k, at.step(n_slots)) {
             if (k < pairs - vblocks) continue;
-            if (!mbar_wait_within(&ctl->full[at.st], at.turn & 1, limit, p.status)) ctl->fail = 1;
+            if (!mbar_wait_within(&ctl->full[at.st], at.turn & 1, limit, p.status)) bad = true;
             unsigned char *base = ring + at.st * kLaSlot;
             const int halves = smin(2, chunks - 2 * (pairs - 1 - k));
             for (int h = 0; h < halves; ++h) {
@@ -676,7 +672,7 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_co
           }
           la_bar(bar);
           if (j > s.tile) {
-            if (!mbar_wait_within(&ctl->pv_done, (n - 1) & 1, limit, p.status)) ctl->fail = 1;
+            if (!mbar_wait_within(&ctl->pv_done, (n - 1) & 1, limit, p.status)) bad = true;
             __syncwarp();
             tc_fence_after();
             for (int c = r0; c < r0 + NB / 2; c += 8) {
@@ -697,7 +693,7 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_co
         }
         // P^T: token lines of NB query rows, swizzled; free once the products
         // of tile n - 1 are done.
-        if (n >= 1 && !mbar_wait_within(&ctl->pv_done, (n - 1) & 1, limit, p.status)) ctl->fail = 1;
+        if (n >= 1 && !mbar_wait_within(&ctl->pv_done, (n - 1) & 1, limit, p.status)) bad = true;
         unsigned char *pb = smem + ly.p;
         const int t0 = quad * 16 + (lane >> 2);
 #pragma unroll
@@ -758,14 +754,14 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_co
         // each group has looked at one half of the columns
         poison = __reduce_min_sync(0xffffffffu, poison);
         if (lane == 0) ctl->poison[warp - 2] = poison;
-        la_bar_all();
-        if (tid == 0 && grp == 0) {
-          for (int w = 1; w < kLaSoftmaxWarps; ++w) poison = smin(poison, ctl->poison[w]);
-          (whole ? p.unit_poison[s.b * p.row_blocks + rb] : p.part_poison[part]) = poison;
-        }
       }
       la_bar(bar);
-      if (!mbar_wait_within(&ctl->pv_done, (n - 1) & 1, limit, p.status)) ctl->fail = 1;
+      if (p.n_query > 1 && tid == 0) {
+        const int *of = ctl->poison + 4 * grp;
+        int2 *to = whole ? p.unit_poison + s.b * p.row_blocks + rb : p.part_poison + part;
+        (grp ? to->y : to->x) = smin(smin(of[0], of[1]), smin(of[2], of[3]));
+      }
+      if (!mbar_wait_within(&ctl->pv_done, (n - 1) & 1, limit, p.status)) bad = true;
       __syncwarp();
       tc_fence_after();
       if (whole) {
@@ -828,9 +824,10 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_co
     LaRing slot, raw;
     int turn = 0;   // the group whose slot is next
     bool ok = true;
+    auto wait = [&](uint64_t *bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait_within(bar, parity & 1, limit, p.status)) != 0; };
     while (ok && walk.next(p, s)) {
       // queries: one warp a row, scaled so that the largest value lies in [2^14, 2^15)
-      if (s.index > 0 && !mbar_wait_within(&ctl->q_empty, (uint32_t)(s.index - 1) & 1, limit, p.status)) break;
+      if (s.index > 0 && !wait(&ctl->q_empty, (uint32_t)(s.index - 1))) break;
       for (int row = dw; row < NB; row += kLaDequantWarps) {
         const bool live = rb * NB + row < p.rows;
         const bf16 *src = p.q + ((int64_t)s.b * p.rows + rb * NB + row) * p.width;
@@ -865,7 +862,7 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_co
       const int tok = (dw % kLaDequantGroup) * 32 + lane;
       for (int j = 0; j < s.n && ok; ++j, raw.step(kLaRawStages)) {
         const int st = raw.st;
-        ok = mbar_wait_within(&ctl->raw_full[st], raw.turn & 1, limit, p.status);
+        ok = wait(&ctl->raw_full[st], raw.turn);
         const unsigned char *src = smem + ly.raw + st * la_raw_bytes(p.width);
         for (int pr = pairs - 1; pr >= 0 && ok; --pr, slot.step(n_slots), turn = (turn + 1) % kGroups) {
           if (turn != my) continue;
@@ -880,7 +877,7 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_co
             code[c] = in ? *reinterpret_cast<const uint4 *>(codes + c * 16) : make_uint4(0u, 0u, 0u, 0u);
             two[c] = in ? *reinterpret_cast<const unsigned short *>(scales + c * 2) : (unsigned short)0;
           }
-          if (slot.turn > 0) ok = mbar_wait_within(&ctl->empty[sl], (slot.turn - 1) & 1, limit, p.status);
+          if (slot.turn > 0) ok = wait(&ctl->empty[sl], slot.turn - 1);
           if (!ok) break;
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
@@ -934,6 +931,7 @@ constexpr int kLcThreads = 128;
 template <int NB, bool FP4>
 __global__ void __launch_bounds__(kLcThreads) latent_combine_kernel(const LatentAttend p, const int cols) {
   __shared__ __align__(16) float sm[kLcThreads / 32], sl[kLcThreads / 32], sacc[kLcThreads / 32][S4R_MAX_LATENT_RANK], f_s[kLcThreads];
+  __shared__ int first_bad[kLcThreads / 32];
   const int row = blockIdx.x % p.rows, b = blockIdx.x / p.rows, rb = row / NB;
   const int64_t at = (int64_t)b * p.rows + row;
   pdl_wait();
@@ -944,9 +942,14 @@ __global__ void __launch_bounds__(kLcThreads) latent_combine_kernel(const Latent
   const int sees = la_length(p, b) - p.n_query + 1 + row / p.n_heads;
   int poison = INT32_MAX;
   if (p.n_query > 1) {
-    if (parts.y <= 1) poison = p.unit_poison[unit];
-    else
-      for (int i = 0; i < parts.y; ++i) poison = smin(poison, p.part_poison[i == 0 ? parts.x : 2 * (parts.x / 2 + i * p.row_blocks)]);
+    for (int i = threadIdx.x; i < parts.y; i += kLcThreads) {
+      const int2 x = parts.y == 1 ? p.unit_poison[unit] : p.part_poison[i == 0 ? parts.x : 2 * (parts.x / 2 + i * p.row_blocks)];
+      poison = smin(poison, smin(x.x, x.y));
+    }
+    poison = __reduce_min_sync(0xffffffffu, poison);
+    if (lane == 0) first_bad[warp] = poison;
+    __syncthreads();
+    poison = smin(smin(first_bad[0], first_bad[1]), smin(first_bad[2], first_bad[3]));
   }
   if (sees > poison) {
     if (blockIdx.y > 0) return;

@@ -354,6 +354,65 @@ def test_latent_attend_infinities_that_only_later_queries_see(n, H):
 
 
 @pytest.mark.parametrize("dt", ["bf16", "fp4"])
+def test_latent_attend_many_query_tokens(dt):
+    """More query tokens than a tile has rows, some of them with nothing to see, and values that only the later ones may
+    see spread over several tiles and parts."""
+    T, H = 150, 3
+    p = latent_problem(dt, [140, 149, 400, 30000], T, H, 96, 16, seed=31)
+    first = {}
+    if dt == "bf16":
+        flat = p["cache"].view(-1, 96)
+        for b, at in ((2, 300), (3, 29900), (3, 29990)):
+            flat[int(p["table"][b, at // 16]) * 16 + at % 16, 20] = math.inf
+            first.setdefault(b, at)
+    d = run_latent(p, 64, 0.1)
+    assert d["status"] == s4r.S4R_OK
+    step = 2.0 ** -8 if dt == "bf16" else 2.0 ** -11
+    for b, n in enumerate(p["lens"]):
+        rows = p["rows"][b].to(DEV)
+        for t in list(range(0, T, 7)) + [T - 1]:
+            sees = n - T + 1 + t
+            if sees > first.get(b, n):
+                assert not torch.isfinite(d["out"][b, t].float()).all(1).any()
+                continue
+            out, lse, ob, lb = latent_attend(p["q"][b, t].double().to(DEV), rows, sees, 64, 0.1, step)
+            assert_within(d["out"][b, t], out, ob, f"request {b} token {t}")
+            assert_within(d["lse"][b, t], lse, lb, f"request {b} token {t}")
+
+
+def test_latent_attend_more_row_blocks_than_multiprocessors():
+    p = latent_problem("bf16", [130, 64], 1, 9601, 64, 16, seed=32)
+    d = run_latent(p, 40, 0.1)
+    assert d["status"] == s4r.S4R_OK
+    check_latent(p, d, 40, 0.1)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp4"])
+def test_cache_beyond_32_bit_offsets(dt):
+    """Rows written to and read from pages behind 2^32 bytes (and 2^32 values in bf16)."""
+    width, page = 576, 64
+    pages = 120000 if dt == "bf16" else 210000
+    shape, kind = ((pages, page, width), BF) if dt == "bf16" else ((pages, page * width * 9 // 16), torch.uint8)
+    cache = torch.empty(shape, dtype=kind, device=DEV)
+    g = torch.Generator().manual_seed(33)
+    n = 200
+    src = torch.randn(n, width, generator=g).to(BF)
+    ids = [pages - 1, 3, pages - 7, pages // 2]
+    slots = torch.tensor([ids[t // page] * page + t % page for t in range(n)], device=DEV)
+    s4r.s4r_latent_write(latents=src.to(DEV), slots=slots, cache=cache, page_size=page)
+    rows = src.double() if dt == "bf16" else quantise(src)[2]
+    q = torch.randn(1, 1, 20, width, generator=g).to(BF)
+    d = dict(q=q.to(DEV), cache=cache, block_table=i32([ids]), lengths=i32([n]), out=torch.empty(1, 1, 20, 512, dtype=BF, device=DEV),
+             lse=torch.empty(1, 1, 20, device=DEV))
+    a = s4r.latent_attend_args(**d, page_size=page, scale=0.05)
+    ws = torch.empty(s4r.s4r_latent_attend_workspace_bytes(a), dtype=torch.uint8, device=DEV)
+    s4r.s4r_workspace_init(ws)
+    s4r.s4r_latent_attend(s4r.latent_attend_args(**d, page_size=page, scale=0.05, workspace=ws))
+    assert s4r.s4r_read_device_status(ws) == s4r.S4R_OK
+    check_latent(dict(q=q, rows=[rows], lens=[n], dt=dt), d, 512, 0.05)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp4"])
 def test_latent_attend_reports_bad_lengths_and_pages(dt):
     p = latent_problem(dt, [100, 50, 20, 64], 1, 4, 64, 16, seed=10)
     good = run_latent(p, 64, 0.2)
@@ -594,6 +653,27 @@ def test_prefill_captured():
         g.replay()
     torch.cuda.synchronize()
     assert torch.equal(d["out"], want)
+
+
+def test_calls_on_two_streams_at_once():
+    """Projection and prefill have no workspace: calls on two streams do not meet."""
+    probs = [prefill_problem([300, 40], [300, 500], 4, 2, 128, 64, 128, seed=k) for k in (7, 8)]
+    runs = [run_prefill(p, 0.1) for p in probs]
+    want = [d["out"].clone() for d in runs]
+    g = torch.Generator().manual_seed(9)
+    x = [torch.randn(400, 8, 128, generator=g).to(BF).to(DEV) for _ in probs]
+    basis = [(torch.randn(8 * 128, 256, generator=g) / 11).to(BF).to(DEV) for _ in probs]
+    out = [torch.empty(400, 8, 256, dtype=BF, device=DEV) for _ in probs]
+    streams = [torch.cuda.Stream() for _ in probs]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for d, s, a, b, o in zip(runs, streams, x, basis, out):
+            s4r.s4r_prefill_attend(d["args"], s)
+            s4r.s4r_latent_project(a, b, o, to_latent=True, stream=s)
+    torch.cuda.synchronize()
+    for d, w, a, b, o in zip(runs, want, x, basis, out):
+        assert torch.equal(d["out"], w)
+        check_project(a.cpu(), b.cpu(), o, 8, 128, 256, True)
 
 
 # ---------------------------------------------------------------- together
