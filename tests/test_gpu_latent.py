@@ -600,6 +600,15 @@ def test_prefill_growing_logits():
     check_prefill(p, run_prefill(p, 0.0), 0.0)
 
 
+@pytest.mark.parametrize("scale", [1.0, -0.5])
+def test_prefill_growing_logits_with_rotary_keys(scale):
+    """The reference maximum is exceeded again and again in tiles that every query sees whole."""
+    p = prefill_problem([300], [1500], 3, 1, 128, 64, 128, seed=22)
+    p["k"] = (p["k"].float() * torch.linspace(0.05, 12, 1500)[:, None, None]).to(BF)
+    check_prefill(p, run_prefill(p, scale), scale)
+    check_prefill(p, run_prefill(p, scale, causal=False), scale, causal=False)
+
+
 def test_prefill_unseen_keys_have_no_influence():
     p = prefill_problem([200, 90], [200, 90], 2, 1, 64, 64, 64, seed=3)
     d = run_prefill(p, 0.1)
