@@ -41,6 +41,14 @@
 // Probabilities are rounded to bf16 (4-bit cache: fp16) for the second
 // product; the sum that divides it is not.
 //
+// Measured (width 576, rank 512): a CTA takes a tile in 1.64 us with 16 heads
+// (together 6.65 TB/s, the rate of a copy), 1.9 us with 64, 2.0 us from 4-bit
+// rows, where shared memory is the limit: fp16 rows are written once and read by
+// two products.  32 ragged requests of 8250 rows on average, 64 heads: 85 us;
+// 8 requests of 32K, 128 heads, two query tokens: 236 us; 4-bit, 5 requests up
+// to 128K, 20 heads: 95 us; one request of 8K, 16 heads: 15.4 us, of which 12
+// are one tile's chain of latencies and the rest the join of 128 parts.
+//
 // Every wait is bounded (umma.cuh); a wait that gives up sets the status word
 // and ends its role, and every other role then runs out too.
 #pragma once
