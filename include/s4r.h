@@ -414,10 +414,11 @@ s4r_status s4r_latent_write(const s4r_latent_write_args *args, void *stream);
 typedef struct {
   int32_t batch;             /* <= S4R_MAX_REQUESTS */
   int32_t n_query;           /* query tokens a request (1: plain decode) */
-  int32_t n_heads;
+  int32_t n_heads;           /* n_query * n_heads <= 65536 */
   int32_t width;             /* values a cache row: rank + rotary part; multiple of 8 (S4R_FP4: 32) */
   int32_t rank;              /* leading values that are attended; multiple of 8, <= width */
-  int32_t page_size, max_pages;
+  int32_t page_size;
+  int32_t max_pages;         /* max_pages * page_size < 2^31 - 64 */
   s4r_dtype cache_dtype;     /* S4R_BF16 or S4R_FP4 */
   int64_t n_pages;           /* >= 1 */
   float scale;               /* of the logits */

@@ -41,7 +41,7 @@ s4r_status latent_attend_shape(const s4r_latent_attend_args *a) {
   if (a->rank % 8 || a->rank > S4R_MAX_LATENT_RANK || a->batch > S4R_MAX_REQUESTS ||
       (int64_t)a->n_query * a->n_heads > INT32_MAX / S4R_MAX_LATENT_WIDTH ||
       (int64_t)a->n_query * a->n_heads * a->batch > INT32_MAX || (int64_t)a->n_query * a->n_heads > 65536 ||
-      (int64_t)a->max_pages * a->page_size > INT32_MAX)
+      (int64_t)a->max_pages * a->page_size > INT32_MAX - kLaTile)
     return S4R_ERR_UNSUPPORTED;
   return S4R_OK;
 }

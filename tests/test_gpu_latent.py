@@ -96,6 +96,13 @@ def test_page_plan_too_few_token_entries_and_a_bad_free_count():
     check_plan(st, *run_plan(st))
 
 
+def test_page_plan_without_requests():
+    st = dict(old=np.zeros(0, dtype=int), new=np.zeros(0, dtype=int), table=np.zeros((0, 3), dtype=int), page=16,
+              free_pages=np.array([4, 5]), free=2, max_tokens=5)
+    for n in (5, 0, 9000):
+        check_plan(st, *run_plan(st, max_tokens=n), n)
+
+
 def test_page_plan_sums_beyond_32_bits():
     st = dict(old=np.array([5, 2 ** 31 - 1, 0]), new=np.array([3, 2 ** 31 - 1, 4]), table=np.full((3, 2), -1), page=16,
               free_pages=np.array([8, 9]), free=2, max_tokens=20)
@@ -281,7 +288,7 @@ def test_latent_attend_pages(page, dt):
 
 
 @pytest.mark.parametrize("dt", ["bf16", "fp4"])
-@pytest.mark.parametrize("lens", [[30000], [9000, 3, 0, 4097], [64 * 148 * 2] * 2, [130] * 300])
+@pytest.mark.parametrize("lens", [[30000], [9000, 3, 0, 4097], [64 * 148 * 2] * 2, [130] * 300, [0], [0] * 200, [1] * 149])
 def test_latent_attend_lengths(lens, dt):
     p = latent_problem(dt, lens, 1, 16, 320, 64, seed=len(lens))
     check_latent(p, run_latent(p, 256, 0.05), 256, 0.05)
@@ -618,6 +625,13 @@ def test_prefill_unseen_keys_have_no_influence():
     e = run_prefill(q, 0.1)
     assert torch.equal(d["out"][:150], e["out"][:150]) and torch.equal(d["out"][200:], e["out"][200:])
     assert torch.equal(d["lse"][:150], e["lse"][:150])
+
+
+def test_prefill_without_any_key():
+    p = prefill_problem([3, 200], [0, 0], 4, 2, 128, 64, 128, seed=23)
+    for causal in (True, False):
+        d = run_prefill(p, 0.1, causal)
+        assert not d["out"].any() and (d["lse"] == -math.inf).all()
 
 
 def test_prefill_strided_keys():

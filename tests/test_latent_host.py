@@ -95,7 +95,8 @@ REFUSALS = {
         (UNSUPPORTED, dict(width=640)), (UNSUPPORTED, dict(cache_dtype=0)), (UNSUPPORTED, dict(cache_dtype=2, width=568)),
         (INVALID, dict(cache_dtype=2, cache_scale=0.0)), (INVALID, dict(scale=float("inf"))), (INVALID, dict(scale=float("nan"))),
         (INVALID, dict(max_pages=0)), (UNSUPPORTED, dict(max_pages=1 << 26)), (UNSUPPORTED, dict(batch=8193)),
-        (UNSUPPORTED, dict(n_query=1 << 20, n_heads=1 << 10)), (INVALID, dict(q=None)), (INVALID, dict(q=0x1002)),
+        (UNSUPPORTED, dict(n_query=1 << 20, n_heads=1 << 10)), (UNSUPPORTED, dict(n_query=1 << 10, n_heads=65)),
+        (UNSUPPORTED, dict(max_pages=(1 << 31) // 64 - 1)), (INVALID, dict(n_pages=0)), (INVALID, dict(q=None)), (INVALID, dict(q=0x1002)),
         (INVALID, dict(cache=None)), (INVALID, dict(block_table=None)), (INVALID, dict(lengths=0x4004)), (INVALID, dict(out=None)),
         (INVALID, dict(lse=0x7004)), (WORKSPACE, dict(workspace=None)), (WORKSPACE, dict(workspace_bytes=8)),
         (WORKSPACE, dict(workspace=0x6008))]),
