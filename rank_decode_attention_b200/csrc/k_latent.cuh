@@ -95,7 +95,9 @@ struct LatentAttend {
   float *part;                               // [2 * CTAs][NB][rank] unscaled partial results
 };
 
-// Query rows a block of the kernel takes, and how many blocks a request has.
+// Query rows a block of the kernel takes: the least that hold a request's (a tile
+// costs 1.64 us with 16, 1.70 with 32, 1.90 with 64), at most 64, which TMEM and
+// shared memory hold next to a tile of 576 columns.
 __host__ __device__ inline int la_block_rows(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
 
 __host__ __device__ constexpr int la_threads(bool fp4) { return 64 + 32 * (kLaSoftmaxWarps + (fp4 ? kLaDequantWarps : 0)); }

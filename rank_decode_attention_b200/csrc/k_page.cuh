@@ -34,7 +34,10 @@ struct PagePlan {
 
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanPerThread = S4R_MAX_REQUESTS / kPlanThreads;
-constexpr int kPlanTokensPerCta = 4096;
+// A token a thread: more CTAs cost less than a longer loop, the commit kernel
+// included (1100 tokens 6.2 us against 6.8 with 4096 tokens a CTA, 6400 tokens 5.8
+// against 8.4, 32000 tokens 5.9 against 7.6).
+constexpr int kPlanTokensPerCta = kPlanThreads;
 inline size_t plan_smem_bytes(int batch) { return 2 * sizeof(int32_t) * (size_t)(batch + 1); }
 
 // Whether a request's counts are legal and its rows fit its table row.
