@@ -294,7 +294,7 @@ s4r_status s4r_latent_project(const s4r_latent_project_args *a, void *stream) {
   if (!a) return S4R_ERR_INVALID_ARG;
   if (a->n_tokens < 0 || a->n_heads <= 0 || a->head_dim <= 0 || a->rank <= 0) return S4R_ERR_INVALID_ARG;
   if (a->head_dim % 8 || a->rank % 8 || a->head_dim > S4R_MAX_HEAD_DIM || a->rank > S4R_MAX_LATENT_RANK ||
-      a->n_tokens > INT32_MAX || a->n_heads > 65535)
+      a->n_tokens > INT32_MAX - 128 || a->n_heads > 65535)   // token coordinates of the last tile stay in 32 bits
     return S4R_ERR_UNSUPPORTED;
   if (a->n_tokens == 0) return S4R_OK;
   const int64_t n_in = a->to_latent ? a->head_dim : a->rank, n_out = a->to_latent ? a->rank : a->head_dim;
@@ -358,7 +358,8 @@ s4r_status s4r_prefill_attend(const s4r_prefill_attend_args *a, void *stream) {
       a->n_heads_q % a->n_heads_kv)
     return S4R_ERR_INVALID_ARG;
   if (a->head_dim % 8 || a->rope_dim % 8 || a->value_dim % 8 || a->head_dim > 128 || a->value_dim > 128 ||
-      a->rope_dim > 64 || a->batch > 65535 || a->n_heads_q > 65535 || a->max_q > 65535 * 2 * kPfTile || a->total_q > INT32_MAX || a->total_k > INT32_MAX)
+      a->rope_dim > 64 || a->batch > 65535 || a->n_heads_q > 65535 || a->max_q > 65535 * 2 * kPfTile || a->total_q > INT32_MAX - 2 * kPfTile ||
+      a->total_k > INT32_MAX - 2 * kPfTile)
     return S4R_ERR_UNSUPPORTED;
   if (a->batch == 0 || a->total_q == 0 || a->max_q == 0) return S4R_OK;
   const void *must[] = {a->q, a->cu_q, a->cu_k, a->out};

@@ -66,7 +66,6 @@ namespace s4r {
 constexpr int kLaTile = 64;                  // tokens a tile
 constexpr int kLaSlot = kLaTile * 128 * 2;   // bytes of a ring slot: 64 tokens x 128 columns
 constexpr int kLaMaxSlots = 12;
-constexpr int kLaMaxPairs = (S4R_MAX_LATENT_WIDTH + 127) / 128;
 constexpr int kLaSmemBudget = 227 * 1024;
 constexpr int kLaSoftmaxWarps = 8;           // two groups of 4, half of the query rows each
 constexpr int kLaDequantWarps = 8;           // groups of kLaDequantGroup take turns at the ring slots

@@ -103,7 +103,7 @@ REFUSALS = {
     "s4r_latent_project": (dict(n_tokens=4), [
         (INVALID, dict(n_tokens=-1)), (INVALID, dict(n_heads=0)), (INVALID, dict(head_dim=0)), (INVALID, dict(rank=0)),
         (UNSUPPORTED, dict(head_dim=60)), (UNSUPPORTED, dict(head_dim=264)), (UNSUPPORTED, dict(rank=520)), (UNSUPPORTED, dict(rank=100)),
-        (UNSUPPORTED, dict(n_heads=70000)), (UNSUPPORTED, dict(n_tokens=1 << 31)), (INVALID, dict(x=None)), (INVALID, dict(x=0x1008)),
+        (UNSUPPORTED, dict(n_heads=70000)), (UNSUPPORTED, dict(n_tokens=1 << 31)), (UNSUPPORTED, dict(n_tokens=(1 << 31) - 100)), (INVALID, dict(x=None)), (INVALID, dict(x=0x1008)),
         (INVALID, dict(basis=None)), (INVALID, dict(out=0x3004)), (INVALID, dict(x_ts=260)), (INVALID, dict(x_hs=-64)),
         (INVALID, dict(x_hs=32)), (INVALID, dict(x_ts=0)), (INVALID, dict(out_hs=0)), (INVALID, dict(out_ts=760)),
         (INVALID, dict(out_hs=184)), (INVALID, dict(out_ts=4))]),
@@ -112,7 +112,7 @@ REFUSALS = {
         (INVALID, dict(rope_dim=-8)), (INVALID, dict(value_dim=0)), (INVALID, dict(max_q=-1)), (INVALID, dict(total_k=-1)),
         (UNSUPPORTED, dict(head_dim=136)), (UNSUPPORTED, dict(head_dim=100)), (UNSUPPORTED, dict(value_dim=256)),
         (UNSUPPORTED, dict(rope_dim=72)), (UNSUPPORTED, dict(rope_dim=4)), (UNSUPPORTED, dict(batch=65536)),
-        (UNSUPPORTED, dict(total_q=1 << 31)), (INVALID, dict(scale=float("nan"))), (INVALID, dict(q=None)), (INVALID, dict(k=None)),
+        (UNSUPPORTED, dict(total_q=1 << 31)), (UNSUPPORTED, dict(total_k=(1 << 31) - 200)), (UNSUPPORTED, dict(max_q=1 << 25)), (INVALID, dict(scale=float("nan"))), (INVALID, dict(q=None)), (INVALID, dict(k=None)),
         (INVALID, dict(v=0x3008)), (INVALID, dict(k_rope=None)), (INVALID, dict(cu_q=None)), (INVALID, dict(cu_k=0x6004)),
         (INVALID, dict(out=None)), (INVALID, dict(lse=0x9004)), (INVALID, dict(k_ts=248)), (INVALID, dict(v_ts=260)),
         (INVALID, dict(k_rope_ts=56))]),
