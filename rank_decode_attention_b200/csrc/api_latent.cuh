@@ -14,6 +14,21 @@ inline int log2_of(int32_t x) {
 // A grid of `want` CTAs, within what a launch takes.
 inline unsigned grid_of(int64_t want, int64_t most) { return (unsigned)smax<int64_t>(1, smin<int64_t>(want, most)); }
 
+// Launch a kernel whose set-up may overlap the end of the kernel before it (it
+// calls pdl_wait before it touches global memory).
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kernel)(P...), unsigned grid, int block, size_t smem, cudaStream_t st, const A &...args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3((unsigned)block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1] = {pdl_attr()};
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 s4r_status page_size_ok(int32_t page_size) {
   if (page_size <= 0) return S4R_ERR_INVALID_ARG;
   return pow2(page_size) && page_size >= 16 && page_size <= S4R_MAX_PAGE_SIZE ? S4R_OK : S4R_ERR_UNSUPPORTED;
@@ -109,8 +124,8 @@ s4r_status latent_attend_launch(const LatentAttend &p, cudaStream_t st) {
   const size_t smem = (size_t)la_layout(NB, p.width, FP4).total;
   cudaError_t err = ensure_smem<latent_attend_kernel<NB, FP4>>(smem);
   if (err != cudaSuccess) return fail("latent_attend_kernel (shared memory)", err);
-  latent_attend_kernel<NB, FP4><<<(unsigned)(p.n_groups * p.row_blocks), la_threads(FP4), smem, st>>>(kv, q, p);
-  if (check_launch("latent_attend_kernel") != S4R_OK) return S4R_ERR_CUDA;
+  err = launch_after(latent_attend_kernel<NB, FP4>, (unsigned)(p.n_groups * p.row_blocks), la_threads(FP4), smem, st, kv, q, p);
+  if (err != cudaSuccess) return fail("latent_attend_kernel", err);
   cudaLaunchConfig_t cfg = {};
   // Few rows with many parts each: their columns go to CTAs of their own (16
   // rows of 128 parts: the whole call 15.6 us against 18.9; 256 rows: the same;
@@ -151,8 +166,8 @@ s4r_status latent_project_launch(const CUtensorMap &mx, const CUtensorMap &mb, c
   const cudaError_t err = ensure_smem<latent_project_kernel<NT>>(kLpSmem);
   if (err != cudaSuccess) return fail("latent_project_kernel (shared memory)", err);
   const unsigned grid = grid_of((int64_t)n_tiles * p.m_tiles, sm_count());
-  latent_project_kernel<NT><<<grid, kLpThreads, kLpSmem, st>>>(mx, mb, mo, p);
-  return check_launch("latent_project_kernel");
+  const cudaError_t rc = launch_after(latent_project_kernel<NT>, grid, kLpThreads, kLpSmem, st, mx, mb, mo, p);
+  return rc == cudaSuccess ? S4R_OK : fail("latent_project_kernel", rc);
 }
 
 template <int KC, int VC>

@@ -312,6 +312,7 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_co
     ctl->n_tiles = 0;
   }
   if (warp == 0) tmem_alloc(&ctl->tmem_base, 512);
+  pdl_wait();   // nothing before this touches memory that another kernel writes
   // This CTA's range of the tile stream: every thread sums a consecutive run
   // of requests, and the one whose run holds the start walks to it.
   {

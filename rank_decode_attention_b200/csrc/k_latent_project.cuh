@@ -76,6 +76,7 @@ latent_project_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_co
     tma_prefetch_desc(&map_o);
   }
   if (warp == 0) tmem_alloc(tmem_slot, 2 * NT);
+  pdl_wait();   // nothing before this touches memory that another kernel writes
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
