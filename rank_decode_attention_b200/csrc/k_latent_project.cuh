@@ -16,8 +16,8 @@
 // next tile is being multiplied.  The weights are K-major when latents are
 // expanded and N-major when queries are absorbed; the descriptors say which.
 //
-// Measured: 64 tokens, 128 heads, 128 -> 512: 7.0 us (3.9 TB/s); 8190 tokens with
-// one latent for 32 heads, 512 -> 128: 30.8 us, 1.12 PFLOP/s, bound by the 384 KB
+// Measured: 64 tokens, 128 heads, 128 -> 512: 6.6 us (4.1 TB/s); 8190 tokens with
+// one latent for 32 heads, 512 -> 128: 30.0 us, 1.14 PFLOP/s, bound by the 384 KB
 // of operands that a 128 x 256 tile takes from L2 (13 TB/s together).
 #pragma once
 #include "umma.cuh"
