@@ -312,7 +312,8 @@ s4r_status s4r_reconstruct(const void *coeffs, int64_t n_rows_total, const void 
  * is row p % page_size of page block_table[b][p / page_size], and
  * slot = page * page_size + row names a row of the whole cache.
  * s4r_page_plan hands out pages and computes slots, s4r_latent_write stores
- * rows.
+ * rows.  Unlike a decode call's first kernel, the kernels of this section read
+ * no input before the work enqueued ahead of them has completed.
  *
  * A page of a S4R_BF16 cache is [page_size][width].  A page of a S4R_FP4
  * cache is page_size * width * 9 / 16 bytes: the codes [page_size][width/2]
