@@ -131,7 +131,7 @@ struct LaControl {
   uint64_t full[kLaMaxSlots], empty[kLaMaxSlots];
   uint64_t raw_full[kLaRawStages], raw_empty[kLaRawStages];
   uint64_t s_full[2], p_full, pv_done;
-  uint64_t q_full, q_empty, o_free, drained;
+  uint64_t q_full[2], q_empty, o_free, drained;
   uint32_t tmem_base;
   int first_b, first_off, n_tiles;   // start of this CTA's range and its length
   int share;                         // tiles of a full range
@@ -165,6 +165,16 @@ struct LaRing {
     }
   }
 };
+
+// The queries of segment `index` arrive on barrier la_query_bar of two, in the
+// phase of parity la_query_parity.  The softmax warps wait for them too, and may
+// be a segment late (they store the end of a unit, or zeros for empty requests,
+// while the products of the next segment run): the queries of segment index + 1
+// may then be complete already.  On one barrier their phase would hide the one
+// waited for; on two by turns the phase that could hide it is that of segment
+// index + 2, whose queries wait for products that need these warps.
+__host__ __device__ inline int la_query_bar(int index) { return index & 1; }
+__host__ __device__ inline uint32_t la_query_parity(int index) { return (uint32_t)(index >> 1) & 1u; }
 
 // The segments of a CTA: consecutive tiles of one request.
 struct LaSegment {
@@ -302,7 +312,7 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_co
     for (int i = 0; i < 2; ++i) mbar_init(&ctl->s_full[i], 1);
     mbar_init(&ctl->p_full, kLaSoftmaxWarps);
     mbar_init(&ctl->pv_done, 1);
-    mbar_init(&ctl->q_full, FP4 ? kLaDequantWarps : 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&ctl->q_full[i], FP4 ? kLaDequantWarps : 1);
     mbar_init(&ctl->q_empty, 1);
     mbar_init(&ctl->drained, 1);
     mbar_init(&ctl->o_free, kLaSoftmaxWarps);
@@ -401,9 +411,10 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_co
       if constexpr (!FP4) {
         if (s.index > 0) ok = wait(&ctl->q_empty, (uint32_t)(s.index - 1));
         if (!ok) break;
-        mbar_expect_if(leader, &ctl->q_full, (uint32_t)(chunks * NB * 128));
+        uint64_t *q_full = &ctl->q_full[la_query_bar(s.index)];
+        mbar_expect_if(leader, q_full, (uint32_t)(chunks * NB * 128));
         for (int c = 0; c < chunks; ++c)
-          tma_load_2d_if(leader, smem + ly.q + c * NB * 128, &map_q, &ctl->q_full, c * 64, s.b * p.rows + rb * NB);
+          tma_load_2d_if(leader, smem + ly.q + c * NB * 128, &map_q, q_full, c * 64, s.b * p.rows + rb * NB);
       }
       for (int j = s.tile; j < s.tile + s.n && ok; ++j) {
         if (left == 0) {   // 32 is a multiple of a tile's boxes
@@ -505,7 +516,7 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_co
       // between units the queries change: finish the last one while they load
       if (due) ok = second();
       due = false;
-      if (ok) ok = wait(&ctl->q_full, (uint32_t)s.index);
+      if (ok) ok = wait(&ctl->q_full[la_query_bar(s.index)], la_query_parity(s.index));
       for (int j = 0; j < s.n && ok; ++j) {
         const uint32_t d = tmem + kStatCols + (n & 1) * NB;
         LaRing first = slot;
@@ -597,7 +608,7 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_co
         tmem_wait_ld();
         if constexpr (FP4) {
           if (j == s.tile) {
-            if (!mbar_wait_within(&ctl->q_full, (uint32_t)s.index & 1, limit, p.status)) bad = true;
+            if (!mbar_wait_within(&ctl->q_full[la_query_bar(s.index)], la_query_parity(s.index), limit, p.status)) bad = true;
 #pragma unroll
             for (int i = 0; i < R; ++i)
               mul[i] = to2 * exp2f((float)-ctl->qexp[s.index & 1][r0 + 8 * (i >> 1) + 2 * (lane & 3) + (i & 1)]);
@@ -866,7 +877,7 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_co
       }
       fence_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&ctl->q_full);
+      if (lane == 0) mbar_arrive(&ctl->q_full[la_query_bar(s.index)]);
       // Ring slots: a group of two warps takes every fourth, a thread one token
       // of it, 128 columns.
       const int tok = (dw % kLaDequantGroup) * 32 + lane;
