@@ -38,8 +38,8 @@
 //              6 significant bits, so fp16 holds the stored values exactly.
 //              Queries become fp16 too, scaled by a power of two per row, exact
 //              over 29 binades below the row's largest value.
-// Probabilities are rounded to bf16 (4-bit cache: fp16) for the second
-// product; the sum that divides it is not.
+// Probabilities are rounded to bf16 (4-bit cache: fp16, in its upper range) for
+// the second product; the sum that divides it is not.
 //
 // Measured (width 576, rank 512): a CTA takes a tile in 1.64 us with 16 heads
 // (together 6.65 TB/s, the rate of a copy), 1.9 us with 64, 2.0 us from 4-bit
@@ -71,7 +71,14 @@ constexpr int kLaSoftmaxWarps = 8;           // two groups of 4, half of the que
 constexpr int kLaDequantWarps = 8;           // groups of kLaDequantGroup take turns at the ring slots
 constexpr int kLaDequantGroup = 2;
 constexpr int kLaRawStages = 2;
-constexpr float kLaLift = 8.0f;              // how far (in powers of two) a logit may exceed the reference
+// How far (in powers of two) the largest logit lies above the reference when the
+// reference moves, and how far a later one may come to lie.  fp16 probabilities
+// (4-bit cache) start at 2^7 and end at 2^15, half of fp16's range: so they keep
+// 11 bits down to 2^-21 of the largest one and are off by at most 2^-32 of it
+// below that (2^-25, half of fp16's smallest step).  bf16 has fp32's range.
+template <bool FP4> struct LaRange {
+  static constexpr float kHead = FP4 ? 7.0f : 0.0f, kLift = kHead + 8.0f;
+};
 
 struct LatentAttend {
   int32_t batch, n_query, n_heads, width, rank, page_size, page_shift, max_pages;
@@ -633,7 +640,7 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_co
           }
         }
 #pragma unroll
-        for (int i = 0; i < R; ++i) over |= fmaxf(y0[i], y1[i]) > m[i] + kLaLift;
+        for (int i = 0; i < R; ++i) over |= fmaxf(y0[i], y1[i]) > m[i] + LaRange<FP4>::kLift;
         // A wait that gave up in one thread ends the group as a whole: the second
         // vote tells it from a moved maximum, so that all threads agree.
         over = la_bar_any(bar, over || bad);
@@ -671,7 +678,7 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_co
           ++slot.turn;
         }
         if (over) {
-          // New reference: the largest logit of each query row so far.
+          // New reference: the largest logit of each query row so far, less kHead.
 #pragma unroll
           for (int i = 0; i < R; ++i) {
             float t = fmaxf(y0[i], y1[i]);
@@ -685,7 +692,7 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_co
             const int row = r0 + 8 * (i >> 1) + 2 * (lane & 3) + (i & 1);
             float t = m[i];
 #pragma unroll
-            for (int w = 0; w < 4; ++w) t = fmaxf(t, ctl->wmax[w][row]);
+            for (int w = 0; w < 4; ++w) t = fmaxf(t, ctl->wmax[w][row] - LaRange<FP4>::kHead);
             const float f = t == m[i] ? 1.0f : exp2f(m[i] - t);   // from -inf: 0
             m[i] = t;
             l[i] *= f;

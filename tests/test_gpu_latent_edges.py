@@ -1,10 +1,15 @@
 """The paged latent operators and prefill attention at rare inputs: where their roles, roundings and special cases meet."""
+import math
+
 import pytest
+import torch
 
 import rank_decode_attention_b200 as s4r
+from latent_reference import HALF_STEP, assert_within, cdiv, latent_attend, pack_page, quantise
 from test_gpu_latent import check_latent, latent_problem, run_latent
 
 pytestmark = pytest.mark.gpu
+BF, DEV = torch.bfloat16, "cuda"
 
 
 # ---------------------------------------------------------------- segments of one tile
@@ -22,3 +27,66 @@ def test_segments_of_one_tile(name, lens, H, dt):
     d = run_latent(p, 64, 0.1)
     assert d["status"] == s4r.S4R_OK
     check_latent(p, d, 64, 0.1)
+
+
+# ---------------------------------------------------------------- probabilities in 16 bits
+
+def fp16_steps(rows, rank):
+    """What the smallest probabilities of a 4-bit cache may be off by, beside their relative rounding (2^-11, counted in
+    latent_attend): the largest one is kept in fp16 as 2^7 at least, so the sum that divides them is 2^7 at least, and
+    none is off by more than half of fp16's smallest step, 2^-25: 2^-32 of the sum, times the values (and 2^-7 of it
+    again for the other roundings on the way)."""
+    return 2.0 ** -32 * (1 + 2.0 ** -7) * rows[:, :rank].abs().sum(0)
+
+@pytest.mark.parametrize("at", [5, 32760])
+def test_fp4_small_probabilities_behind_a_dominant_row(at):
+    """One row takes nearly all of the weight and is 0 in the columns looked at; the 2^15 others weigh 2^-X of it each.
+    All requests name the same pages, one request a multiprocessor, so that no part has a maximum of its own.
+
+    Looked at: the error that fp16_steps allows, which is small beside what the others weigh together."""
+    n, width, rank, page, H = 1 << 15, 64, 64, 1024, 10
+    g = torch.Generator().manual_seed(at)
+    rows = torch.randn(n, width, generator=g).abs().to(BF)
+    rows[:, 0] = 0.0
+    rows[at] = 0.0
+    rows[at, 0] = 6.0                                         # a scale of 1: exact
+    q = torch.zeros(1, 1, H, width)
+    q[0, 0, :, 0] = torch.tensor([0.0, 14, 18, 20, 22, 24, 24.5, 25, 25.5, 26]) / 6   # X, with logits in powers of two
+    codes, scales, exact = quantise(rows)
+    cache = torch.stack([pack_page(codes[i:i + page], scales[i:i + page]) for i in range(0, n, page)])
+    B = torch.cuda.get_device_properties(0).multi_processor_count
+    p = dict(q=q.to(BF).expand(B, 1, H, width).contiguous(), cache=cache, page=page, dt="fp4", lens=[n] * B,
+             table=torch.arange(n // page, dtype=torch.int32).expand(B, -1).contiguous())
+    scale = math.log(2)
+    d = run_latent(p, rank, scale)
+    assert d["status"] == s4r.S4R_OK
+    exact = exact.to(DEV)
+    out, lse, ob, lb = latent_attend(p["q"][0, 0].double().to(DEV), exact, n, rank, scale, HALF_STEP[torch.float16])
+    ob = ob + fp16_steps(exact, rank)
+    for b in (0, 1, B // 2, B - 1):
+        assert_within(d["out"][b, 0], out, ob, f"request {b}")
+        assert_within(d["lse"][b, 0], lse, lb, f"request {b}")
+
+
+def test_fp4_growing_logits():
+    """4-bit rows whose logits rise by far more than the reference is allowed to lag, so that it moves again and again."""
+    lens, H, width, rank, page = [700, 2500], 40, 192, 128, 32
+    p = latent_problem("fp4", lens, 1, H, width, page, seed=3)
+    g = torch.Generator().manual_seed(4)
+    for b, n in enumerate(lens):
+        rows = (torch.randn(n, width, generator=g) * torch.linspace(0.1, 8, n)[:, None]).to(BF)
+        codes, scales, p["rows"][b] = quantise(rows)
+        for k in range(cdiv(n, page)):
+            c, s = torch.zeros(page, width, dtype=torch.uint8), torch.zeros(page, width // 16, dtype=torch.uint8)
+            m = min(page, n - k * page)
+            c[:m], s[:m] = codes[k * page:k * page + m], scales[k * page:k * page + m]
+            c[m:], s[m:] = 15, 0x7e                           # the largest values behind the length
+            p["cache"][int(p["table"][b, k])] = pack_page(c, s)
+    for scale in (1.0, -0.7):
+        d = run_latent(p, rank, scale)
+        assert d["status"] == s4r.S4R_OK
+        for b, n in enumerate(lens):
+            rows = p["rows"][b].to(DEV)
+            out, lse, ob, lb = latent_attend(p["q"][b, 0].double().to(DEV), rows, n, rank, scale, HALF_STEP[torch.float16])
+            assert_within(d["out"][b, 0], out, ob + fp16_steps(rows, rank), f"out of request {b}")
+            assert_within(d["lse"][b, 0], lse, lb, f"lse of request {b}")
