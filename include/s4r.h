@@ -401,11 +401,12 @@ s4r_status s4r_latent_write(const s4r_latent_write_args *args, void *stream);
  * token t sees rows 0 .. lengths[b] - n_query + t.  For every head h
  *   z_i = scale * q[b][t][h] . row_i,  p = softmax(z),
  *   out[b][t][h] = sum_i p_i row_i[0 .. rank-1],  lse[b][t][h] = log sum_i e^{z_i}.
- * A query token that sees no row gets out = 0, lse = -infinity.  What lies in
- * rows that a query does not see (NaN and infinities included) has no
- * influence.  fp32 statistics and accumulation; probabilities are rounded to
- * 16 bits (bf16 next to bf16 rows, fp16 next to 4-bit ones: those below 2^-21
- * of the largest one to 2^-32 of it) for the value product only.
+ * A query token that sees no row, or none whose logit is above -infinity, gets
+ * out = 0, lse = -infinity.  What lies in rows that a query does not see (NaN
+ * and infinities included) has no influence.  fp32 statistics and
+ * accumulation; probabilities are rounded to 16 bits (bf16 next to bf16 rows,
+ * fp16 next to 4-bit ones: those below 2^-21 of the largest one to 2^-32 of it)
+ * for the value product only.
  * Device status (S4R_ERR_DEVICE): a length outside [0, max_pages *
  * page_size] (clamped), a page id outside [0, n_pages) among a request's
  * pages (not read); S4R_ERR_TIMEOUT as elsewhere.  The outputs

@@ -991,8 +991,9 @@ __global__ void __launch_bounds__(kLcThreads) latent_combine_kernel(const Latent
       float z = 0.0f;
       for (int c = lane; c < p.width; c += 32) z = fmaf(to_f(p.q[at * p.width + c]), latent_value<FP4>(p, page, r, c), z);
       z = warp_sum(z) * p.scale;
+      // logits of -infinity weigh nothing, also while there is no other one
       const float top = fmaxf(m, z);
-      const float f = m == -CUDART_INF_F ? 0.0f : expf(m - top), e = expf(z - top);
+      const float f = m == -CUDART_INF_F ? 0.0f : expf(m - top), e = expf(z - (top == -CUDART_INF_F ? 0.0f : top));
       l = l * f + e;
       m = top;
 #pragma unroll
@@ -1008,15 +1009,20 @@ __global__ void __launch_bounds__(kLcThreads) latent_combine_kernel(const Latent
 #pragma unroll
     for (int k = 0; k < kCols; ++k) sacc[warp][k * 32 + lane] = acc[k];
     __syncthreads();
-    float top = -CUDART_INF_F, sum = 0.0f;
+    float top = -CUDART_INF_F, sum = 0.0f, f[W];
     for (int w = 0; w < W; ++w) top = fmaxf(top, sm[w]);
-    for (int w = 0; w < W; ++w) sum += sl[w] == 0.0f ? 0.0f : expf(sm[w] - top) * sl[w];
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      f[w] = sm[w] == -CUDART_INF_F ? 0.0f : expf(sm[w] - top);
+      sum += f[w] * sl[w];   // a NaN in a warp's sum stays one
+    }
     for (int c = threadIdx.x; c < p.rank; c += kLcThreads) {
       float o = 0.0f;
-      for (int w = 0; w < W; ++w) o += sl[w] == 0.0f ? 0.0f : expf(sm[w] - top) * sacc[w][c];
-      p.out[at * p.rank + c] = from_f<bf16>(sees > 0 ? o / sum : 0.0f);
+#pragma unroll
+      for (int w = 0; w < W; ++w) o += f[w] * sacc[w][c];
+      p.out[at * p.rank + c] = from_f<bf16>(sum == 0.0f ? 0.0f : o / sum);
     }
-    if (p.lse && threadIdx.x == 0) p.lse[at] = sees > 0 ? top + logf(sum) : -CUDART_INF_F;
+    if (p.lse && threadIdx.x == 0) p.lse[at] = top + logf(sum);   // no weight at all: -infinity
     return;
   }
   if (parts.y <= 1) return;

@@ -90,3 +90,27 @@ def test_fp4_growing_logits():
             out, lse, ob, lb = latent_attend(p["q"][b, 0].double().to(DEV), rows, n, rank, scale, HALF_STEP[torch.float16])
             assert_within(d["out"][b, 0], out, ob + fp16_steps(rows, rank), f"out of request {b}")
             assert_within(d["lse"][b, 0], lse, lb, f"lse of request {b}")
+
+
+# ---------------------------------------------------------------- logits of minus infinity
+
+@pytest.mark.parametrize("n", [2, 3, 5, 40, 3000, 30000])
+def test_latent_keys_of_weight_zero_in_rows_computed_again(n):
+    """Row 0 has a logit of minus infinity for every query, and so has the newest row, whose infinity lies beside value
+    columns that only the last query may see: its rows are computed again one by one, and both rows weigh nothing."""
+    H, width, rank = 5, 192, 160
+    p = latent_problem("bf16", [n, 100], 2, H, width, 32, seed=n)
+    p["q"][..., 170], p["q"][..., 180] = -0.5, 0.5
+    flat = p["cache"].view(-1, width)
+    for at, col, bad in ((0, 180, -math.inf), (n - 1, 170, math.inf)):
+        flat[int(p["table"][0, at // 32]) * 32 + at % 32, col] = bad
+    live = p["rows"][0][1:n - 1]
+    d = run_latent(p, rank, 0.05)
+    assert d["status"] == s4r.S4R_OK
+    for t in range(2):        # both queries see rows 1 .. n - 2, and rows that weigh nothing
+        out, lse, ob, lb = latent_attend(p["q"][0, t].double(), live, n - 2, rank, 0.05, HALF_STEP[BF])
+        assert_within(d["out"][0, t].cpu(), out, ob, f"out of token {t}")
+        assert_within(d["lse"][0, t].cpu(), lse, lb, f"lse of token {t}")
+    for t in range(2):
+        out, lse, ob, lb = latent_attend(p["q"][1, t].double(), p["rows"][1], 99 + t, rank, 0.05, HALF_STEP[BF])
+        assert_within(d["out"][1, t].cpu(), out, ob, "the other request")
