@@ -469,8 +469,9 @@ s4r_status s4r_latent_project(const s4r_latent_project_args *args, void *stream)
  *   z = scale * (q[:head_dim] . k + q[head_dim:] . k_rope),
  *   out = softmax(z) . v, lse = log sum e^z
  * k_rope is one row a key token for all heads (rope_dim == 0: none).  A query
- * that sees no key gets out = 0, lse = -infinity.  fp32 statistics and
- * accumulation, probabilities rounded to bf16 for the value product only.
+ * that sees no key, or none whose logit is above -infinity, gets out = 0, lse =
+ * -infinity.  fp32 statistics and accumulation, probabilities rounded to bf16
+ * for the value product only.
  * Rows of out and lse outside every sequence are left as they are.
  * max_q must be at least the longest query count; it only sizes the launch.
  * Device status (the library-wide word, s4r_read_device_status(NULL, .)):

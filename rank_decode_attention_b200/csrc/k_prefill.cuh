@@ -143,8 +143,9 @@ __device__ __noinline__ void prefill_row(const PrefillAttend &p, const PrefillSe
       if (lane + 32 * c < p.rope) z = fmaf(qr[c], to_f(p.k_rope[row * p.k_rope_ts + lane + 32 * c]), z);
     z = warp_sum(z) * p.scale;
     const float top = fmaxf(m, z);
+    // logits of -infinity weigh nothing, also while there is no other one
     const float f = m == -CUDART_INF_F ? 0.0f : expf(m - top);
-    const float e = expf(z - top);
+    const float e = expf(z - (top == -CUDART_INF_F ? 0.0f : top));
     l = l * f + e;
     m = top;
 #pragma unroll
@@ -154,8 +155,8 @@ __device__ __noinline__ void prefill_row(const PrefillAttend &p, const PrefillSe
   bf16 *o = p.out + ((s.q0 + i) * p.hq + h) * (int64_t)p.vdim;
 #pragma unroll
   for (int c = 0; c < 4; ++c)
-    if (lane + 32 * c < p.vdim) o[lane + 32 * c] = from_f<bf16>(sees > 0 ? acc[c] / l : 0.0f);
-  if (lane == 0 && p.lse) p.lse[(s.q0 + i) * p.hq + h] = sees > 0 ? m + logf(l) : -CUDART_INF_F;
+    if (lane + 32 * c < p.vdim) o[lane + 32 * c] = from_f<bf16>(l == 0.0f ? 0.0f : acc[c] / l);
+  if (lane == 0 && p.lse) p.lse[(s.q0 + i) * p.hq + h] = m + logf(l);   // no weight at all: -infinity
 }
 
 // KC, VC: 64-column chunks of a key (rotary part included) and of a value; as

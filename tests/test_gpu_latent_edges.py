@@ -6,7 +6,7 @@ import torch
 
 import rank_decode_attention_b200 as s4r
 from latent_reference import HALF_STEP, assert_within, cdiv, latent_attend, pack_page, quantise
-from test_gpu_latent import check_latent, latent_problem, run_latent
+from test_gpu_latent import check_latent, check_prefill, latent_problem, prefill_problem, run_latent, run_prefill
 
 pytestmark = pytest.mark.gpu
 BF, DEV = torch.bfloat16, "cuda"
@@ -114,3 +114,34 @@ def test_latent_keys_of_weight_zero_in_rows_computed_again(n):
     for t in range(2):
         out, lse, ob, lb = latent_attend(p["q"][1, t].double(), p["rows"][1], 99 + t, rank, 0.05, HALF_STEP[BF])
         assert_within(d["out"][1, t].cpu(), out, ob, "the other request")
+
+
+@pytest.mark.parametrize("rope", [0, 64])
+@pytest.mark.parametrize("n", [40, 300])
+def test_prefill_keys_of_weight_zero_in_rows_computed_again(n, rope):
+    """Key 0 has a logit of minus infinity for every query; a value on the diagonal is infinite, so the queries that see
+    it are computed again one by one.  Only the column of the infinity is infinite."""
+    p = prefill_problem([n, 70], [n, 70], 4, 2, 64, rope, 64, seed=n + rope)
+    p["q"][..., 9] = 0.5
+    p["k"][0, :, 9] = -math.inf
+    late = n - 7
+    p["v"][late, :, 3] = math.inf
+    d = run_prefill(p, 0.1)
+    assert s4r.s4r_read_device_status(None) == s4r.S4R_OK
+    assert (d["out"][0] == 0).all() and (d["lse"][0] == -math.inf).all()        # sees key 0 only
+    clean = {k: (v.clone() if isinstance(v, torch.Tensor) else v) for k, v in p.items()}
+    clean["k"][0], clean["v"][late, :, 3] = 0.0, 0.0
+    clean["q"] = clean["q"][1:]                                                  # queries 1 .. with keys 1 ..
+    clean["k"], clean["v"] = clean["k"][1:], clean["v"][1:]
+    if rope:
+        clean["k_rope"] = clean["k_rope"][1:]
+    clean["cu_q"] = clean["cu_k"] = [0, n - 1, n + 69]
+    got = dict(out=d["out"][1:].clone(), lse=d["lse"][1:])
+    assert (got["out"][late - 1:n - 1, :, 3] == math.inf).all()
+    got["out"][late - 1:n - 1, :, 3] = 0.0
+    # the column of the infinity: compared where no query sees it
+    keep = got["out"].clone()
+    want = run_prefill(clean, 0.1)
+    got["out"][late - 1:n - 1, :, 3] = want["out"][late - 1:n - 1, :, 3]
+    check_prefill(clean, got, 0.1)
+    assert torch.isfinite(keep).all()
