@@ -812,8 +812,10 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_co
             uint32_t q[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const uint32_t t = pack_bf16(__uint_as_float(w[c][2 * i]) * f[8 * c + 2 * i],
-                                           __uint_as_float(w[c][2 * i + 1]) * f[8 * c + 2 * i + 1]);
+              // a row without any weight is 0, whatever its values are
+              const float f0 = f[8 * c + 2 * i], f1 = f[8 * c + 2 * i + 1];
+              const uint32_t t = pack_bf16(f0 == 0.0f ? 0.0f : __uint_as_float(w[c][2 * i]) * f0,
+                                           f1 == 0.0f ? 0.0f : __uint_as_float(w[c][2 * i + 1]) * f1);
               const uint32_t x = __shfl_xor_sync(0xffffffffu, t, 1);
               q[i] = up1 ? __byte_perm(x, t, 0x7632) : __byte_perm(t, x, 0x5410);   // row 2 i + lane % 2
             }

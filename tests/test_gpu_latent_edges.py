@@ -116,6 +116,24 @@ def test_latent_keys_of_weight_zero_in_rows_computed_again(n):
         assert_within(d["out"][1, t].cpu(), out, ob, "the other request")
 
 
+@pytest.mark.parametrize("n", [1, 2, 40])
+def test_latent_rows_without_any_weight(n):
+    """Every row has an infinity, so that no logit of the even heads is above minus infinity: they get 0 and minus infinity,
+    infinite values or not.  The odd heads' logits are NaN or infinite, and so are they; the other request stays exact."""
+    H, width = 6, 64
+    p = latent_problem("bf16", [n, 90], 1, H, width, 16, seed=n)
+    p["q"][0, 0, 0::2, 11], p["q"][0, 0, 1::2, 11] = -0.5, 0.5
+    flat = p["cache"].view(-1, width)
+    for at in range(n):
+        flat[int(p["table"][0, at // 16]) * 16 + at % 16, 11] = math.inf
+    d = run_latent(p, width, 0.2)
+    assert d["status"] == s4r.S4R_OK
+    assert (d["out"][0, 0, 0::2] == 0).all() and (d["lse"][0, 0, 0::2] == -math.inf).all()
+    assert torch.isnan(d["out"][0, 0, 1::2]).all()
+    out, lse, ob, lb = latent_attend(p["q"][1, 0].double(), p["rows"][1], 90, width, 0.2, HALF_STEP[BF])
+    assert_within(d["out"][1, 0].cpu(), out, ob)
+
+
 @pytest.mark.parametrize("rope", [0, 64])
 @pytest.mark.parametrize("n", [40, 300])
 def test_prefill_keys_of_weight_zero_in_rows_computed_again(n, rope):
