@@ -50,9 +50,19 @@ __host__ __device__ inline int32_t plan_need(int32_t old, int32_t add, int32_t m
   if (!plan_fits(old, add, max_pages, ps)) return 0;
   return (int32_t)((((int64_t)old + add + ps - 1) >> page_shift) - (((int64_t)old + ps - 1) >> page_shift));
 }
+// Whether a legal request is served, by the pages it needs, the running demand
+// up to it and the free pages.  The demand says nothing about the need: where it
+// is held at its largest value, neighbours are equal.
+__host__ __device__ inline bool plan_served(int32_t need, uint32_t demand, int32_t free_pages) {
+  return need == 0 || demand <= (uint32_t)free_pages;
+}
+// What a sum is held at: tokens fit their 32-bit offsets; pages stay above any
+// count of free ones.
+__host__ __device__ inline int32_t plan_hold_tokens(long long x) { return (int32_t)smin<long long>(x, INT32_MAX); }
+__host__ __device__ inline uint32_t plan_hold_pages(long long x) { return (uint32_t)smin<long long>(x, UINT32_MAX); }
 // Largest i in [0, n] with a[i] <= x, for ascending a and a[0] <= x: the last
 // of several equal entries, so that empty requests own nothing.
-__host__ __device__ inline int plan_find(const int32_t *a, int n, int32_t x) {
+template <typename T> __host__ __device__ inline int plan_find(const T *a, int n, T x) {
   int lo = 0, hi = n;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -63,8 +73,8 @@ __host__ __device__ inline int plan_find(const int32_t *a, int n, int32_t x) {
 }
 
 // Exclusive prefix sums of tokens and pages over the batch, batch + 1 entries
-// each, sums beyond 2^31 - 1 held there (64-bit inside).
-__device__ inline void plan_scan(const PagePlan &p, int32_t *s_tok, int32_t *s_pg) {
+// each, 64-bit inside.
+__device__ inline void plan_scan(const PagePlan &p, int32_t *s_tok, uint32_t *s_pg) {
   __shared__ long long w_tok[32], w_pg[32];
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const int per = (p.batch + kPlanThreads - 1) / kPlanThreads;   // <= kPlanPerThread
@@ -111,14 +121,17 @@ __device__ inline void plan_scan(const PagePlan &p, int32_t *s_tok, int32_t *s_p
   }
   __syncthreads();
   long long et = it - st + (warp ? w_tok[warp - 1] : 0), ep = ip - sp + (warp ? w_pg[warp - 1] : 0);
-  if (t == 0) s_tok[0] = s_pg[0] = 0;
+  if (t == 0) {
+    s_tok[0] = 0;
+    s_pg[0] = 0u;
+  }
 #pragma unroll
   for (int i = 0; i < kPlanPerThread; ++i) {
     if (i < per && b0 + i < p.batch) {
       et += tok[i];
       ep += pg[i];
-      s_tok[b0 + i + 1] = (int32_t)smin<long long>(et, INT32_MAX);
-      s_pg[b0 + i + 1] = (int32_t)smin<long long>(ep, INT32_MAX);
+      s_tok[b0 + i + 1] = plan_hold_tokens(et);
+      s_pg[b0 + i + 1] = plan_hold_pages(ep);
     }
   }
   __syncthreads();
@@ -134,7 +147,7 @@ __device__ __forceinline__ int32_t plan_free(const PagePlan &p, bool report) {
 
 // The per-request results: lengths_out, free_count_out.  They may overwrite
 // the inputs, so every read of those is behind the caller's barrier.
-__device__ inline void plan_commit(const PagePlan &p, const int32_t *s_pg, int32_t free_pages, int32_t taken) {
+__device__ inline void plan_commit(const PagePlan &p, const uint32_t *s_pg, int32_t free_pages, int32_t taken) {
   const int per = (p.batch + kPlanThreads - 1) / kPlanThreads;
   const int b0 = threadIdx.x * per;
 #pragma unroll
@@ -143,7 +156,7 @@ __device__ inline void plan_commit(const PagePlan &p, const int32_t *s_pg, int32
     if (i < per && b < p.batch) {
       const int32_t old = p.lengths[b], add = p.new_tokens[b];
       const bool fits = plan_fits(old, add, p.max_pages, p.page_size);
-      const bool served = fits && (s_pg[b + 1] == s_pg[b] || s_pg[b + 1] <= free_pages);
+      const bool served = fits && plan_served(plan_need(old, add, p.max_pages, p.page_shift), s_pg[b + 1], free_pages);
       if (!served) set_status(p.status, kDevStatusCheck);
       p.lengths_out[b] = served ? old + add : old;
     }
@@ -153,14 +166,15 @@ __device__ inline void plan_commit(const PagePlan &p, const int32_t *s_pg, int32
 
 __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PagePlan p) {
   extern __shared__ int32_t plan_smem[];
-  int32_t *s_tok = plan_smem, *s_pg = plan_smem + p.batch + 1;
+  int32_t *s_tok = plan_smem;
+  uint32_t *s_pg = reinterpret_cast<uint32_t *>(plan_smem + p.batch + 1);
   if (gridDim.x > 1) pdl_trigger();   // the commit kernel may take its sums; it waits for this grid before it writes
   plan_scan(p, s_tok, s_pg);
   const int32_t total = s_tok[p.batch];
   const int32_t free_pages = plan_free(p, blockIdx.x == 0);
   // Requests are served as long as the running demand fits, so what they take
   // is the largest running demand that does.
-  const int32_t taken = s_pg[plan_find(s_pg, p.batch, free_pages)];
+  const int32_t taken = (int32_t)s_pg[plan_find(s_pg, p.batch, (uint32_t)free_pages)];
   if (blockIdx.x == 0) {
     for (int i = threadIdx.x; i <= p.batch; i += kPlanThreads) p.cu_tokens[i] = s_tok[i];
     if (threadIdx.x == 0 && total > p.max_tokens) set_status(p.status, kDevStatusCheck);
@@ -169,7 +183,7 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PagePlan 
   // New table entries.  They are never read here: the tokens below take the
   // ids of new pages from the free list.
   for (int64_t j = first; j < taken; j += step) {
-    const int b = plan_find(s_pg, p.batch, (int32_t)j);
+    const int b = plan_find(s_pg, p.batch, (uint32_t)j);
     const int32_t have = (int32_t)(((int64_t)p.lengths[b] + p.page_size - 1) >> p.page_shift);
     p.block_table[(int64_t)b * p.max_pages + have + (j - s_pg[b])] = p.free_pages[free_pages - 1 - j];
   }
@@ -180,11 +194,12 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PagePlan 
       req = plan_find(s_tok, p.batch, (int32_t)t);
       const int32_t old = p.lengths[req], add = p.new_tokens[req];
       pos = (int32_t)(old + (t - s_tok[req]));
-      const int32_t d0 = s_pg[req], d1 = s_pg[req + 1];
-      if (plan_fits(old, add, p.max_pages, p.page_size) && (d0 == d1 || d1 <= free_pages)) {
+      const uint32_t d0 = s_pg[req], d1 = s_pg[req + 1];
+      if (plan_fits(old, add, p.max_pages, p.page_size) &&
+          plan_served(plan_need(old, add, p.max_pages, p.page_shift), d1, free_pages)) {
         const int32_t have = (int32_t)(((int64_t)old + p.page_size - 1) >> p.page_shift), at = pos >> p.page_shift;
         const int32_t page = at < have ? p.block_table[(int64_t)req * p.max_pages + at]
-                                       : p.free_pages[free_pages - 1 - (d0 + at - have)];
+                                       : p.free_pages[free_pages - 1 - ((int32_t)d0 + at - have)];
         slot = (int64_t)page * p.page_size + (pos & (p.page_size - 1));
       }
     }
@@ -202,10 +217,11 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PagePlan 
 // wait for all of them in a launch of their own.
 __global__ void __launch_bounds__(kPlanThreads) page_commit_kernel(const PagePlan p) {
   extern __shared__ int32_t plan_smem[];
-  int32_t *s_tok = plan_smem, *s_pg = plan_smem + p.batch + 1;
+  int32_t *s_tok = plan_smem;
+  uint32_t *s_pg = reinterpret_cast<uint32_t *>(plan_smem + p.batch + 1);
   plan_scan(p, s_tok, s_pg);
   const int32_t free_pages = plan_free(p, false);
-  const int32_t taken = s_pg[plan_find(s_pg, p.batch, free_pages)];
+  const int32_t taken = (int32_t)s_pg[plan_find(s_pg, p.batch, (uint32_t)free_pages)];
   __syncthreads();
   pdl_wait();
   plan_commit(p, s_pg, free_pages, taken);

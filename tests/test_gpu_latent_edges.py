@@ -6,7 +6,8 @@ import torch
 
 import rank_decode_attention_b200 as s4r
 from latent_reference import HALF_STEP, assert_within, cdiv, latent_attend, pack_page, quantise
-from test_gpu_latent import check_latent, check_prefill, latent_problem, prefill_problem, run_latent, run_prefill
+from test_gpu_latent import (check_latent, check_prefill, i32, latent_problem, prefill_problem, run_latent, run_prefill,
+                             status_words)
 
 pytestmark = pytest.mark.gpu
 BF, DEV = torch.bfloat16, "cuda"
@@ -163,3 +164,23 @@ def test_prefill_keys_of_weight_zero_in_rows_computed_again(n, rope):
     got["out"][late - 1:n - 1, :, 3] = want["out"][late - 1:n - 1, :, 3]
     check_prefill(clean, got, 0.1)
     assert torch.isfinite(keep).all()
+
+
+# ---------------------------------------------------------------- page plan
+
+def test_page_plan_demand_beyond_32_bits():
+    """17 requests ask for 2^27 - 1 pages each; behind them one page is not there either, though the sum of the pages
+    no longer fits 31 bits.  A request that opens no page is served all the same."""
+    page, cols = 16, 2 ** 27 - 1
+    B = 19
+    old, new = [0] * B, [page * cols] * 17 + [5, 3]
+    old[18] = 1
+    table = torch.empty(B, cols, dtype=torch.int32, device=DEV)
+    table[18, 0] = 6
+    lengths, free = i32(old), i32([3])
+    cu, slots, w = i32([0] * (B + 1)), torch.zeros(20, dtype=torch.int64, device=DEV), status_words()
+    s4r.s4r_page_plan(lengths=lengths, new_tokens=i32(new), block_table=table, free_pages=i32([7, 8, 9]), free_count=free,
+                      lengths_out=lengths, free_count_out=free, cu_tokens=cu, slots=slots, page_size=page, status_workspace=w)
+    assert s4r.s4r_read_device_status(w) == s4r.S4R_ERR_DEVICE
+    assert lengths.tolist() == [0] * 18 + [4] and int(free) == 3
+    assert (slots == -1).all()
