@@ -563,17 +563,17 @@ prefill_attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
         __syncwarp();
       }
       if (i < rows && p.lse) p.lse[at] = l == 0.0f ? -CUDART_INF_F : (m + log2f(l)) * 0.6931471805599453f;
-      const int poison = *reinterpret_cast<volatile int *>(&ctl->poison);
-      if (poison != INT32_MAX)
-        for (int r = 0; r < 32; ++r) {
-          const int row = q0 + t * kPfTile + quad * 32 + r;
-          if (row < rows && (int64_t)s.nk - s.nq + row >= poison) prefill_row(p, s, row, h);
-        }
     }
   }
   tc_fence_before();
   __syncthreads();
   if (warp == 0) tmem_dealloc(tmem, 512);
+  // Rows that see an infinity which others must not see are written once more:
+  // behind the barrier, which orders both writes and the note of the first key.
+  const int poison = ctl->poison;
+  if (poison != INT32_MAX)
+    for (int r = warp; r < 2 * kPfTile; r += kPfThreads / 32)
+      if (q0 + r < rows && (int64_t)s.nk - s.nq + q0 + r >= poison) prefill_row(p, s, q0 + r, h);
 }
 
 }  // namespace s4r
