@@ -28,7 +28,8 @@ int main(int argc, char **argv) {
   std::vector<uint32_t> demand(1, 0u);
   long long sum = 0;
   for (int i = 2; i < argc; ++i) demand.push_back(plan_hold_pages(sum += atoll(argv[i])));
-  for (int i = 2; i < argc; ++i) printf("served %d\n", plan_served(atoi(argv[i]), demand[i - 1], free_pages) ? 1 : 0);
+  for (int i = 2; i < argc; ++i)   // need pages of 16 tokens, 5 tokens of a page held already
+    printf("served %d\n", plan_served(5, atoi(argv[i]) ? 16 * atoi(argv[i]) : 11, 1 << 27, 4, demand[i - 1], free_pages) ? 1 : 0);
   printf("taken %u\n", demand[plan_find(demand.data(), argc - 2, (uint32_t)free_pages)]);
   return 0;
 }
