@@ -796,6 +796,9 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_co
         float f[NB / 2];   // of this group's rows
 #pragma unroll
         for (int i = 0; i < NB / 2; ++i) f[i] = ctl->fac[r0 + i];
+        bool none = false;   // a row without any weight is 0, whatever its values are
+#pragma unroll
+        for (int i = 0; i < NB / 2; ++i) none |= f[i] == 0.0f;
         const bool up1 = lane & 1, up2 = lane & 2, up4 = lane & 4;
         bf16 *out = p.out + (row0 + r0 + (lane & 7)) * p.rank + quad * 32 + (lane & 24);
         for (int vb = 0; vb < vblocks; ++vb, out += 128) {
@@ -804,6 +807,11 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_co
 #pragma unroll
           for (int c = 0; c < NB / 16; ++c) tmem_ld8(tmem + lanes + vb * NB + r0 + 8 * c, w[c]);
           tmem_wait_ld();
+          if (none) {
+#pragma unroll
+            for (int i = 0; i < NB / 2; ++i)
+              if (f[i] == 0.0f) w[i / 8][i % 8] = 0u;
+          }
           const bool in = vb * 128 + quad * 32 + (lane & 24) < p.rank;
 #pragma unroll
           for (int c = 0; c < NB / 16; ++c) {
@@ -812,10 +820,8 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_co
             uint32_t q[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              // a row without any weight is 0, whatever its values are
-              const float f0 = f[8 * c + 2 * i], f1 = f[8 * c + 2 * i + 1];
-              const uint32_t t = pack_bf16(f0 == 0.0f ? 0.0f : __uint_as_float(w[c][2 * i]) * f0,
-                                           f1 == 0.0f ? 0.0f : __uint_as_float(w[c][2 * i + 1]) * f1);
+              const uint32_t t = pack_bf16(__uint_as_float(w[c][2 * i]) * f[8 * c + 2 * i],
+                                           __uint_as_float(w[c][2 * i + 1]) * f[8 * c + 2 * i + 1]);
               const uint32_t x = __shfl_xor_sync(0xffffffffu, t, 1);
               q[i] = up1 ? __byte_perm(x, t, 0x7632) : __byte_perm(t, x, 0x5410);   // row 2 i + lane % 2
             }
