@@ -160,6 +160,19 @@ __device__ __forceinline__ int32_t la_tiles(int32_t len) { return (len + kLaTile
 // Tiles of a range, of `total`.
 __host__ __device__ inline long long la_share(long long total, int n_groups) { return (total + n_groups - 1) / n_groups; }
 
+// The slots of the partial sums of a unit: its parts, from the record (first
+// slot, count) of the CTA with its first tile.  Part 0 lies in the slot of the
+// record, the others in the first slot of the CTAs behind it, row_blocks apart.
+__host__ __device__ inline int la_part_slot(int first, int i, int row_blocks) {
+  return i == 0 ? first : 2 * (first / 2 + i * row_blocks);
+}
+// Whether a record names slots that exist.  After a wait that gave up it may be
+// what the memory held before the call.
+__host__ __device__ inline bool la_parts_ok(int first, int count, int n_groups, int row_blocks) {
+  const uint32_t ctas = (uint32_t)(n_groups * row_blocks), more = (uint32_t)count - 1u;
+  return (more < (uint32_t)n_groups) & ((uint32_t)first < 2u * ctas) & ((uint32_t)first / 2u + more * (uint32_t)row_blocks < ctas);
+}
+
 // A place in a ring of n slots and the parity of its turn (no divisions: the
 // single-warp roles are bound by the instructions they issue).
 struct LaRing {
@@ -972,14 +985,15 @@ __global__ void __launch_bounds__(kLcThreads) latent_combine_kernel(const Latent
   const int64_t at = (int64_t)b * p.rows + row;
   pdl_wait();
   const int unit = b * p.row_blocks + rb;
-  const int2 parts = p.units[unit];
+  int2 parts = p.units[unit];
+  if (!la_parts_ok(parts.x, parts.y, p.n_groups, p.row_blocks)) parts.y = 1;   // a wait gave up, and the status says so
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   constexpr int W = kLcThreads / 32, kCols = S4R_MAX_LATENT_RANK / 32;
   const int sees = la_length(p, b) - p.n_query + 1 + row / p.n_heads;
   int poison = INT32_MAX;
   if (p.n_query > 1) {
     for (int i = threadIdx.x; i < parts.y; i += kLcThreads) {
-      const int2 x = parts.y == 1 ? p.unit_poison[unit] : p.part_poison[i == 0 ? parts.x : 2 * (parts.x / 2 + i * p.row_blocks)];
+      const int2 x = parts.y == 1 ? p.unit_poison[unit] : p.part_poison[la_part_slot(parts.x, i, p.row_blocks)];
       poison = smin(poison, smin(x.x, x.y));
     }
     poison = __reduce_min_sync(0xffffffffu, poison);
@@ -1034,11 +1048,10 @@ __global__ void __launch_bounds__(kLcThreads) latent_combine_kernel(const Latent
     return;
   }
   if (parts.y <= 1) return;
-  // Part 0 lies in slot parts.x, the others in the first slot of the CTAs
-  // behind it, row_blocks CTAs apart.  Statistics first, a thread a part; then the warps share out the
-  // parts, a lane adding up 4 neighbouring columns of every 128.
+  // Statistics first, a thread a part; then the warps share out the parts, a
+  // lane adding up 4 neighbouring columns of every 128.
   const int r = row - rb * NB;
-  auto slot_of = [&](int i) { return (int64_t)(i == 0 ? parts.x : 2 * (parts.x / 2 + i * p.row_blocks)) * NB + r; };
+  auto slot_of = [&](int i) { return (int64_t)la_part_slot(parts.x, i, p.row_blocks) * NB + r; };
   float top = -CUDART_INF_F;
   for (int i = threadIdx.x; i < parts.y; i += kLcThreads) top = fmaxf(top, p.ml[slot_of(i)].x);
   top = warp_max(top);

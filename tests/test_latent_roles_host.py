@@ -3,6 +3,7 @@
   * The barrier and parity that a role waits on for the queries of a segment: a role that is up to one segment late must
     still find them complete, one that is early must not.
   * Which requests of a page plan are served, when the pages they ask for exceed 31 and 32 bits.
+  * The slots that a unit's record of its parts may name, whatever the record holds.
 """
 import os
 import shutil
@@ -22,6 +23,26 @@ using namespace s4r;
 int main(int argc, char **argv) {
   if (argc == 1) {
     for (int i = 0; i < 64; ++i) printf("query %d %d %u\n", i, la_query_bar(i), la_query_parity(i));
+    return 0;
+  }
+  if (argc == 5 && argv[1][0] == 'p') {   // p groups row_blocks seed: every legal record, then random ones
+    const int groups = atoi(argv[2]), blocks = atoi(argv[3]);
+    const long long slots = 2LL * groups * blocks;
+    srand(atoi(argv[4]));
+    for (int c = 0; c < groups * blocks; ++c)
+      for (int second = 0; second < 2; ++second)
+        for (int n = 1; c / blocks + n <= groups; ++n)
+          if (!la_parts_ok(2 * c + second, n, groups, blocks)) printf("refused %d %d\n", 2 * c + second, n);
+    for (int i = 0; i < 2000000; ++i) {
+      const int mask = 1 << (rand() % 31);
+      int first = (int)((unsigned)rand() * 3u) % mask, n = (int)((unsigned)rand() * 5u) % mask;
+      if (rand() % 4 == 0) first = -first;
+      if (rand() % 4 == 0) n = -n;
+      if (i < 4) first = i & 1 ? INT32_MAX : INT32_MIN, n = i & 2 ? INT32_MAX : 1;
+      if (!la_parts_ok(first, n, groups, blocks)) continue;
+      for (int k = 0; k < n; ++k)
+        if (la_part_slot(first, k, blocks) < 0 || la_part_slot(first, k, blocks) >= slots) printf("outside %d %d\n", first, n);
+    }
     return 0;
   }
   const int32_t free_pages = atoi(argv[1]);   // then the pages that each request needs
@@ -77,3 +98,9 @@ def test_the_plan_serves_while_the_demand_fits(host, needs, free):
             taken = demand
     assert host("served", free, *needs) == want
     assert host("taken", free, *needs) == [[taken]]
+
+
+@pytest.mark.parametrize("groups,blocks", [(148, 1), (74, 2), (1, 1024), (5, 3), (1, 1)])
+def test_records_of_parts(host, groups, blocks):
+    assert host("refused", "p", groups, blocks, 1) == []
+    assert host("outside", "p", groups, blocks, 1) == []
