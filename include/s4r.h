@@ -520,8 +520,9 @@ s4r_status s4r_clear_device_status(void *workspace, void *stream);
  *   - limit_cycles: the limit in SM clock cycles (<= 0: the default, about
  *     2 s);
  *   - unreachable_barrier: when non-zero, the grid-wide barrier of the
- *     latent-scoring kernel waits for one arrival more than its grid has,
- *     so it always runs out after the limit.
+ *     latent-scoring kernel waits for one arrival more than its grid has, and
+ *     s4r_latent_attend's second product for probabilities that never come,
+ *     so they always run out after the limit.
  * It synchronises the device (cudaMemcpyToSymbol); do not call it while
  * other work of this library runs.  S4R_ERR_CUDA if the copy fails. */
 s4r_status s4r_debug_waits(int64_t limit_cycles, int32_t unreachable_barrier);

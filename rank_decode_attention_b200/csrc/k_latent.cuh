@@ -50,7 +50,8 @@
 // are one tile's chain of latencies and the rest the join of 128 parts.
 //
 // Every wait is bounded (umma.cuh); a wait that gives up sets the status word
-// and ends its role, and every other role then runs out too.
+// and ends its role, and every other role then runs out too.  The producer and
+// the issuer end only when what they issued has ended.
 #pragma once
 #include <cuda_fp4.h>
 #include <cuda_fp8.h>
@@ -139,6 +140,7 @@ struct LaControl {
   uint64_t raw_full[kLaRawStages], raw_empty[kLaRawStages];
   uint64_t s_full[2], p_full, pv_done;
   uint64_t q_full[2], q_empty, o_free, drained;
+  uint64_t never;                    // no one arrives (s4r_debug_waits)
   uint32_t tmem_base;
   int first_b, first_off, n_tiles;   // start of this CTA's range and its length
   int share;                         // tiles of a full range
@@ -318,6 +320,7 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_co
   const int chunks = (p.width + 63) / 64, pairs = (chunks + 1) / 2, vblocks = (p.rank + 127) / 128;
   const int n_slots = p.slots, rb = blockIdx.x % p.row_blocks;   // this CTA's block of query rows
   const long long limit = wait_limit();
+  const bool unreachable = wait_unreachable();
   constexpr int kStatCols = 4 * NB;   // S^T behind the four blocks of O^T
 
   if (threadIdx.x == 0) {
@@ -335,6 +338,7 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_co
     for (int i = 0; i < 2; ++i) mbar_init(&ctl->q_full[i], FP4 ? kLaDequantWarps : 1);
     mbar_init(&ctl->q_empty, 1);
     mbar_init(&ctl->drained, 1);
+    mbar_init(&ctl->never, 1);
     mbar_init(&ctl->o_free, kLaSoftmaxWarps);
     mbar_fence_init();
     ctl->first_b = 0;
@@ -399,6 +403,7 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_co
     LaWalk walk(ctl);
     LaSegment s;
     LaRing slot, raw;
+    int asked = -1;   // the last segment whose queries were copied
     bool ok = true;
     const uint32_t leader = elect_one();
     const int box = smin(p.page_size, kLaTile), box_shift = smin(p.page_shift, 6), per_tile = kLaTile >> box_shift;
@@ -432,6 +437,7 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_co
         if (s.index > 0) ok = wait(&ctl->q_empty, (uint32_t)(s.index - 1));
         if (!ok) break;
         uint64_t *q_full = &ctl->q_full[la_query_bar(s.index)];
+        asked = s.index;
         mbar_expect_if(leader, q_full, (uint32_t)(chunks * NB * 128));
         for (int c = 0; c < chunks; ++c)
           tma_load_2d_if(leader, smem + ly.q + c * NB * 128, &map_q, q_full, c * 64, s.b * p.rows + rb * NB);
@@ -483,15 +489,18 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_co
         }
       }
     }
-    if (!ok) {   // let the copies in flight land before the CTA ends
-      if constexpr (!FP4) {
-        for (int i = 0; i < n_slots; ++i)
-          if (slot.turn > 0 || i < slot.st) wait(&ctl->full[i], slot.turn - (i < slot.st ? 0 : 1));
-      } else {
-        for (int i = 0; i < kLaRawStages; ++i)
-          if (raw.turn > 0 || i < raw.st) wait(&ctl->raw_full[i], raw.turn - (i < raw.st ? 0 : 1));
-      }
+    // Shared memory goes with the CTA: let the copies in flight land, whichever
+    // role gave up.
+    auto land = [&](uint64_t *bar, uint32_t parity) { mbar_wait_within(bar, parity & 1, kWaitCycles, p.status); };
+    if constexpr (!FP4) {
+      if (asked >= 0) land(&ctl->q_full[la_query_bar(asked)], la_query_parity(asked));
+      for (int i = 0; i < n_slots; ++i)
+        if (slot.turn > 0 || i < slot.st) land(&ctl->full[i], slot.turn - (i < slot.st ? 0 : 1));
+    } else {
+      for (int i = 0; i < kLaRawStages; ++i)
+        if (raw.turn > 0 || i < raw.st) land(&ctl->raw_full[i], raw.turn - (i < raw.st ? 0 : 1));
     }
+    __syncwarp();
   } else if (warp == 1) {
     // ---------------------------------------------------------- MMA issuer
     // The whole warp walks along and one lane issues under a predicate.  What
@@ -511,13 +520,14 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_co
     const uint64_t p_desc = sdesc_sw128(smem_u32(smem + ly.p), kLaTile * 128, 1024);
     auto wait = [&](uint64_t *bar, uint32_t parity) { return __shfl_sync(0xffffffffu, (int)mbar_wait_within(bar, parity & 1, limit, p.status), 0) != 0; };
     auto ready = [&](uint64_t *bar, uint32_t parity) { return __shfl_sync(0xffffffffu, (int)mbar_test(bar, parity & 1), 0) != 0; };
+    uint64_t *const p_full = unreachable ? &ctl->never : &ctl->p_full;
     LaRing slot;
     uint32_t n = 0;                      // tiles so far
     bool due = false, due_first = false; // the tile before waits for its second product; it is its unit's first
     LaRing due_slot;                     // its first slot of values
     int due_index = 0;
     auto second = [&]() {   // O^T += V^T P^T of tile n - 1
-      if (!wait(&ctl->p_full, n - 1)) return false;
+      if (!wait(p_full, n - 1)) return false;
       if (due_first && due_index > 0 && !wait(&ctl->o_free, (uint32_t)(due_index - 1))) return false;
       tc_fence_after();
       for (int vb = vblocks - 1; vb >= 0; --vb, due_slot.step(n_slots)) {
@@ -544,7 +554,7 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_co
           // The second product of the tile before goes first once its
           // probabilities are there (its slots are then free early), or if
           // this slot comes free only with it.
-          if (due && (ready(&ctl->p_full, n - 1) ||
+          if (due && (ready(p_full, n - 1) ||
                       (slot.turn > 0 && (slot.turn - 1 > due_slot.turn || (slot.turn - 1 == due_slot.turn && slot.st >= due_slot.st))))) {
             ok = second();
             due = false;
@@ -578,11 +588,11 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_co
       }
     }
     if (ok && due) ok = second();
-    if (!ok) {   // TMEM and shared memory go with the CTA: let the products in flight end
-      umma_commit_if(leader, &ctl->drained);
-      mbar_wait_within(&ctl->drained, 0, kWaitCycles, p.status);
-      __syncwarp();
-    }
+    // TMEM and shared memory go with the CTA: let the products in flight end,
+    // whichever role gave up.
+    umma_commit_if(leader, &ctl->drained);
+    mbar_wait_within(&ctl->drained, 0, kWaitCycles, p.status);
+    __syncwarp();
   } else if (warp < 2 + kLaSoftmaxWarps) {
     // ------------------------------------------------------------- softmax
     // Two groups of four warps, each with half of the query rows and all tokens;
@@ -946,6 +956,7 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_co
           if (lane == 0) mbar_arrive(&ctl->full[sl]);
         }
         __syncwarp();
+        if (!ok) break;   // the copies into this stage may still be under way: it is not free
         if (lane == 0) mbar_arrive(&ctl->raw_empty[st]);
       }
     }

@@ -18,13 +18,18 @@ __device__ uint32_t g_device_status;
 
 // Limit of every bounded wait in SM cycles, and a switch that makes the
 // latent-scoring kernel's grid barrier wait for one arrival more than its grid
-// has.  Only s4r_debug_waits changes them (so that tests can make a wait run
-// out); they are read once per wait, on its slow path.
+// has and latent attention's second product wait for probabilities that never
+// come.  Only s4r_debug_waits changes them (so that tests can make a wait run
+// out); they are read once per wait, on its slow path, or once per kernel.
 __device__ long long g_wait_limit = kWaitCycles;
 __device__ uint32_t g_barrier_unreachable = 0u;
 __device__ __forceinline__ long long wait_limit() {
   const long long v = *reinterpret_cast<volatile long long *>(&g_wait_limit);
   return v > 0 ? v : kWaitCycles;
+}
+
+__device__ __forceinline__ bool wait_unreachable() {
+  return *reinterpret_cast<volatile uint32_t *>(&g_barrier_unreachable) != 0u;
 }
 
 __device__ __forceinline__ uint32_t smem_u32(const void *p) {

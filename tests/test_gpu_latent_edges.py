@@ -184,3 +184,37 @@ def test_page_plan_demand_beyond_32_bits():
     assert s4r.s4r_read_device_status(w) == s4r.S4R_ERR_DEVICE
     assert lengths.tolist() == [0] * 18 + [4] and int(free) == 3
     assert (slots == -1).all()
+
+
+# ---------------------------------------------------------------- waits that give up
+
+@pytest.fixture
+def waits():
+    yield s4r.s4r_debug_waits
+    torch.cuda.synchronize()
+    s4r.s4r_debug_waits(0, False)
+    s4r.s4r_clear_device_status(None)
+
+
+@pytest.mark.parametrize("limit,unreachable", [(2_000_000, True), (1, True), (1, False), (2000, False)])
+@pytest.mark.parametrize("dt", ["bf16", "fp4"])
+@pytest.mark.parametrize("lens,T,H", [([5000, 20, 0, 300], 1, 20), ([9000, 70] + [1] * 400, 2, 64)])
+def test_latent_attend_waits_that_give_up(waits, lens, T, H, dt, limit, unreachable):
+    """The call ends and reports it, on a workspace that held another call's sums; the next call is right again."""
+    p = latent_problem(dt, lens, T, H, 192, 32, seed=len(lens))
+    good = run_latent(p, 160, 0.1)
+    check_latent(p, good, 160, 0.1)
+    g = torch.Generator(device=DEV).manual_seed(1)
+    ws = good["ws"].view(torch.int32)
+    for fill in ("sums", "whole numbers"):
+        ws[64:] = (torch.randn(ws.numel() - 64, generator=g, device=DEV).view(torch.int32) if fill == "sums" else
+                   torch.randint(-2 ** 31, 2 ** 31, (ws.numel() - 64,), generator=g, device=DEV).int())
+        waits(limit, unreachable)
+        s4r.s4r_latent_attend(good["args"])
+        status = s4r.s4r_read_device_status(good["ws"])
+        waits(0, False)
+        assert status == s4r.S4R_ERR_TIMEOUT or (status == s4r.S4R_OK and not unreachable)
+        s4r.s4r_clear_device_status(good["ws"])
+        s4r.s4r_latent_attend(good["args"])
+        assert s4r.s4r_read_device_status(good["ws"]) == s4r.S4R_OK
+        check_latent(p, good, 160, 0.1)
