@@ -521,8 +521,8 @@ s4r_status s4r_clear_device_status(void *workspace, void *stream);
  *     2 s);
  *   - unreachable_barrier: when non-zero, the grid-wide barrier of the
  *     latent-scoring kernel waits for one arrival more than its grid has, and
- *     s4r_latent_attend's second product for probabilities that never come,
- *     so they always run out after the limit.
+ *     the second products of s4r_latent_attend and s4r_prefill_attend for
+ *     probabilities that never come, so they always run out after the limit.
  * It synchronises the device (cudaMemcpyToSymbol); do not call it while
  * other work of this library runs.  S4R_ERR_CUDA if the copy fails. */
 s4r_status s4r_debug_waits(int64_t limit_cycles, int32_t unreachable_barrier);

@@ -22,7 +22,9 @@
 //              hide them from the rows that must not see them); rows that do see
 //              one are computed again one by one at the end.
 // CTAs start with the queries that see most keys, all heads of them, so that
-// the short ones fill up the end.
+// the short ones fill up the end.  Every wait is bounded (umma.cuh); after one
+// that gave up every role runs out, the producer and the issuer when what they
+// issued has ended.
 //
 // Measured: one prompt of 8192, 16 heads, 128 + 64 | 128: 301 us, 1.14 PFLOP/s;
 // six prompts of 33 to 2900 behind a prefix of 517, 32 over 8 heads, 128 | 128:
@@ -87,6 +89,7 @@ struct PfControl {
   uint64_t full[kPfMaxSlots], empty[kPfMaxSlots];
   uint64_t landed[kPfMaxSlots];   // a chunk of V that is looked after first
   uint64_t q_full, drained;
+  uint64_t never;                 // no one arrives (s4r_debug_waits)
   uint64_t s_full[2], p_full[2], pv_done[2];
   uint32_t tmem_base;
   int poison;   // first key whose values some rows must not see
@@ -197,6 +200,7 @@ prefill_attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
   }
   const int n_all = smax(n_t[0], n_t[1]);
   const long long limit = wait_limit();
+  const bool unreachable = wait_unreachable();
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < n_slots; ++i) {
@@ -206,6 +210,7 @@ prefill_attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
     }
     mbar_init(&ctl->q_full, 1);
     mbar_init(&ctl->drained, 1);
+    mbar_init(&ctl->never, 1);
     for (int t = 0; t < 2; ++t) {
       mbar_init(&ctl->s_full[t], 1);
       mbar_init(&ctl->p_full[t], 4);
@@ -236,6 +241,8 @@ prefill_attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
     const uint32_t leader = elect_one();
     bool ok = n_all > 0;
     PfRing slot;
+    // by slot: whether its last copy arrives on `landed`, and how many did, modulo 2
+    uint32_t on_landed = 0, landed = 0;
     if (ok) {
       mbar_expect_if(leader, &ctl->q_full, (uint32_t)(2 * kc) * kPfChunk);
       for (int t = 0; t < 2; ++t)
@@ -251,13 +258,16 @@ prefill_attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
       for (int c = 0; c < kc && ok; ++c, slot.step(n_slots)) {
         if (slot.turn > 0) ok = wait(&ctl->empty[slot.st], slot.turn - 1);
         if (!ok) break;
+        on_landed &= ~(1u << slot.st);
         mbar_expect_if(leader, &ctl->full[slot.st], kPfChunk);
         if (c < nope) tma_load_3d_if(leader, ring + slot.st * kPfChunk, &map_k, &ctl->full[slot.st], c * 64, g, row);
         else tma_load_3d_if(leader, ring + slot.st * kPfChunk, &map_kr, &ctl->full[slot.st], (c - nope) * 64, 0, row);
       }
       if (ok && vc == 2 && slot.st == n_slots - 1) {   // the two chunks of V lie side by side: skip the last slot
         if (slot.turn > 0) ok = wait(&ctl->empty[slot.st], slot.turn - 1);
-        if (ok && leader) mbar_arrive(&ctl->full[slot.st]);
+        if (!ok) break;
+        on_landed &= ~(1u << slot.st);
+        if (leader) mbar_arrive(&ctl->full[slot.st]);
         slot.step(n_slots);
       }
       const bool touch = touched(j);
@@ -265,22 +275,31 @@ prefill_attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
         if (slot.turn > 0) ok = wait(&ctl->empty[slot.st], slot.turn - 1);
         if (!ok) break;
         uint64_t *bar = touch ? &ctl->landed[slot.st] : &ctl->full[slot.st];
+        on_landed = (on_landed & ~(1u << slot.st)) | ((uint32_t)touch << slot.st);
+        landed ^= (uint32_t)touch << slot.st;
         mbar_expect_if(leader, bar, kPfChunk);
         tma_load_3d_if(leader, ring + slot.st * kPfChunk, &map_v, bar, c * 64, g, row);
       }
     }
-    if (!ok && n_all > 0) {   // let the copies in flight land before the CTA ends
-      wait(&ctl->q_full, 0);
-      for (int i = 0; i < n_slots; ++i)
-        if (slot.turn > 0 || i < slot.st) wait(&ctl->full[i], slot.turn - (i < slot.st ? 0 : 1));
+    // Shared memory goes with the CTA: let the copies in flight land, whichever
+    // role gave up.
+    auto land = [&](uint64_t *bar, uint32_t parity) { mbar_wait_within(bar, parity & 1, kWaitCycles, nullptr); };
+    if (n_all > 0) {
+      land(&ctl->q_full, 0);
+      for (int i = 0; i < n_slots; ++i) {
+        if (on_landed >> i & 1) land(&ctl->landed[i], (landed >> i) + 1);
+        else if (slot.turn > 0 || i < slot.st) land(&ctl->full[i], slot.turn - (i < slot.st ? 0 : 1));
+      }
     }
+    __syncwarp();
   } else if (warp == 1) {
     // ---------------------------------------------------------- MMA issuer
     const uint32_t leader = elect_one();
     const uint32_t id_s = idesc_bf16_f32(128, 128, 0, 0), id_o = idesc_bf16_f32(128, 64 * vc, 0, 1);
     const uint64_t q_desc = sdesc_sw128(smem_u32(smem), 16, 1024), k_desc = sdesc_sw128(smem_u32(ring), 16, 1024);
     const uint64_t v_desc = sdesc_sw128(smem_u32(ring), kPfChunk, 1024);
-    bool ok = true;   // after a wait that gave up the others do not wait, and the walk ends
+    bool ok = true;   // after a wait that gave up nothing more is issued: a slot whose copy is under way must not be released
+    uint64_t *const p_full = unreachable ? &ctl->never : ctl->p_full;   // then of tile 0 alone
     auto until = [&](uint64_t *bar, uint32_t parity) {
       if (ok) ok = wait(bar, parity);
       tc_fence_after();
@@ -292,6 +311,7 @@ prefill_attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
       const uint32_t d = tmem + t * 128;
       for (int c = 0; c < kc; ++c, at.step(n_slots)) {
         if (first) until(&ctl->full[at.st], at.turn);
+        if (!ok) return;
         const uint64_t a = q_desc + (uint32_t)(t * kc + c) * (kPfChunk >> 4), k = k_desc + (uint32_t)at.st * (kPfChunk >> 4);
         umma_f16_if(leader, d, a, k, id_s, c > 0);
 #pragma unroll
@@ -301,9 +321,10 @@ prefill_attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
       umma_commit_if(leader, &ctl->s_full[t]);
     };
     auto values = [&](int t, int j, bool first, bool last) {
-      until(&ctl->p_full[t], (uint32_t)j);
+      until(p_full + (unreachable ? 0 : t), (uint32_t)j);
       if (first)
         for (int c = 0; c < vc; ++c) until(&ctl->full[vp.st + c], vp.turn);
+      if (!ok) return;
       const uint64_t v = v_desc + (uint32_t)vp.st * (kPfChunk >> 4);
       const uint32_t d = tmem + 256 + t * 128, a = tmem + t * 128;
       umma_f16_ts_if(leader, d, a, v, id_o, j > 0);
@@ -325,6 +346,7 @@ prefill_attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
         for (int c = 0; c < kc; ++c) vp.step(n_slots);
         if (vc == 2 && vp.st == n_slots - 1) {
           until(&ctl->full[vp.st], vp.turn);
+          if (!ok) break;
           umma_commit_if(leader, &ctl->empty[vp.st]);
           vp.step(n_slots);
         }
@@ -339,11 +361,11 @@ prefill_attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
         if (j + 1 < mine) scores(t, t == 0 || j + 1 >= other, t == 1 || j + 1 >= other);
       }
     }
-    if (!ok) {   // TMEM and shared memory go with the CTA: let the products in flight end
-      umma_commit_if(leader, &ctl->drained);
-      mbar_wait_within(&ctl->drained, 0, kWaitCycles, nullptr);
-      __syncwarp();
-    }
+    // TMEM and shared memory go with the CTA: let the products in flight end,
+    // whichever role gave up.
+    umma_commit_if(leader, &ctl->drained);
+    mbar_wait_within(&ctl->drained, 0, kWaitCycles, nullptr);
+    __syncwarp();
   } else if (warp >= 10) {
     // ------------------------------------------------ chunks of V seen in part
     const int c = warp - 10;
@@ -534,6 +556,7 @@ prefill_attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl->p_full[t]);
     }
+    tmem_wait_ld();   // a wait that gave up may have left a load under way
     if (ok && n_t[t] > 0) ok = wait(&ctl->pv_done[t], (uint32_t)(n_t[t] - 1));
     tc_fence_after();
     if (ok) {

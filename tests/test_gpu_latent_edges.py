@@ -218,3 +218,20 @@ def test_latent_attend_waits_that_give_up(waits, lens, T, H, dt, limit, unreacha
         s4r.s4r_latent_attend(good["args"])
         assert s4r.s4r_read_device_status(good["ws"]) == s4r.S4R_OK
         check_latent(p, good, 160, 0.1)
+
+
+@pytest.mark.parametrize("limit,unreachable", [(2_000_000, True), (1, True), (1, False), (2000, False)])
+@pytest.mark.parametrize("dim,rope,vdim", [(128, 64, 128), (64, 0, 64), (128, 0, 128), (64, 0, 128)])
+def test_prefill_waits_that_give_up(waits, dim, rope, vdim, limit, unreachable):
+    p = prefill_problem([700, 40, 1], [900, 40, 3000], 4, 2, dim, rope, vdim, seed=dim + rope + vdim)
+    good = run_prefill(p, 0.1)
+    check_prefill(p, good, 0.1)
+    waits(limit, unreachable)
+    s4r.s4r_prefill_attend(good["args"])
+    status = s4r.s4r_read_device_status(None)
+    waits(0, False)
+    assert status == s4r.S4R_ERR_TIMEOUT or (status == s4r.S4R_OK and not unreachable)
+    s4r.s4r_clear_device_status(None)
+    s4r.s4r_prefill_attend(good["args"])
+    assert s4r.s4r_read_device_status(None) == s4r.S4R_OK
+    check_prefill(p, good, 0.1)
