@@ -447,7 +447,8 @@ s4r_status s4r_latent_attend(const s4r_latent_attend_args *args, void *stream);
  *   to_latent == 0: out[t][h][d] = sum_j x[t][h][j] B_h[d][j]   (expand latents)
  * x_hs == 0 lets all heads share one x row a token (expanding keys or values
  * from a token's latent).  Strides are in elements, multiples of 8; out rows
- * must not overlap one another or the inputs. */
+ * must not overlap one another or the inputs.  Device status: only
+ * S4R_ERR_TIMEOUT, in the library-wide word (s4r_read_device_status(NULL, .)). */
 typedef struct {
   int64_t n_tokens;
   int32_t n_heads, head_dim, rank;  /* multiples of 8; head_dim <= S4R_MAX_HEAD_DIM, rank <= S4R_MAX_LATENT_RANK */
@@ -520,9 +521,10 @@ s4r_status s4r_clear_device_status(void *workspace, void *stream);
  *   - limit_cycles: the limit in SM clock cycles (<= 0: the default, about
  *     2 s);
  *   - unreachable_barrier: when non-zero, the grid-wide barrier of the
- *     latent-scoring kernel waits for one arrival more than its grid has, and
- *     the second products of s4r_latent_attend and s4r_prefill_attend for
- *     probabilities that never come, so they always run out after the limit.
+ *     latent-scoring kernel waits for one arrival more than its grid has, the
+ *     second products of s4r_latent_attend and s4r_prefill_attend for
+ *     probabilities, and the results of s4r_latent_project for accumulators
+ *     that never come, so they always run out after the limit.
  * It synchronises the device (cudaMemcpyToSymbol); do not call it while
  * other work of this library runs.  S4R_ERR_CUDA if the copy fails. */
 s4r_status s4r_debug_waits(int64_t limit_cycles, int32_t unreachable_barrier);

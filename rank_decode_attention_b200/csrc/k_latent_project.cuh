@@ -13,7 +13,9 @@
 // N = NT) into one of two accumulators, warps 2-5 round a finished accumulator
 // to bf16 into swizzled shared memory and store it with TMA (32 tokens x 64
 // columns a copy; rows and columns outside the tensor are clipped), while the
-// next tile is being multiplied.  The weights are K-major when latents are
+// next tile is being multiplied.  Every wait is bounded (umma.cuh); after one
+// that gave up every role runs out, the producer and the issuer when what they
+// issued has ended.  The weights are K-major when latents are
 // expanded and N-major when queries are absorbed; the descriptors say which.
 //
 // Measured: 64 tokens, 128 heads, 128 -> 512: 6.6 us (4.1 TB/s); 8190 tokens with
@@ -56,6 +58,7 @@ latent_project_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_co
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drained + 1);
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const long long limit = wait_limit();
+  const bool unreachable = wait_unreachable();
   const int nk = (p.n_in + 63) / 64;
   const int64_t tiles = (int64_t)p.m_tiles * p.n_tiles;
   const int head_tiles = (p.head_groups + C::kGroups - 1) / C::kGroups;
@@ -134,9 +137,11 @@ latent_project_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_co
         }
       }
     }
-    if (!ok)   // let the copies in flight land before the CTA ends
-      for (int i = 0; i < C::kStages; ++i)
-        if (turn > 0 || i < st) wait(&full[i], turn - (i < st ? 0 : 1));
+    // Shared memory goes with the CTA: let the copies in flight land, whichever
+    // role gave up.
+    for (int i = 0; i < C::kStages; ++i)
+      if (turn > 0 || i < st) mbar_wait_within(&full[i], (turn - (i < st ? 0 : 1)) & 1, kWaitCycles, nullptr);
+    __syncwarp();
   } else if (warp == 1) {
     const uint32_t leader = elect_one();
     bool ok = true;
@@ -165,13 +170,13 @@ latent_project_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_co
           ++turn;
         }
       }
-      if (ok) umma_commit_if(leader, &acc_full[acc]);
+      if (ok && !unreachable) umma_commit_if(leader, &acc_full[acc]);
     }
-    if (!ok) {   // TMEM and shared memory go with the CTA: let the products in flight end
-      umma_commit_if(leader, drained);
-      mbar_wait_within(drained, 0, kWaitCycles, nullptr);
-      __syncwarp();
-    }
+    // TMEM and shared memory go with the CTA: let the products in flight end,
+    // whichever role gave up.
+    umma_commit_if(leader, drained);
+    mbar_wait_within(drained, 0, kWaitCycles, nullptr);
+    __syncwarp();
   } else {
     const int quad = warp & 3;
     unsigned char *mine = staging + (warp - 2) * 2 * 4096;

@@ -18,8 +18,8 @@ __device__ uint32_t g_device_status;
 
 // Limit of every bounded wait in SM cycles, and a switch that makes the
 // latent-scoring kernel's grid barrier wait for one arrival more than its grid
-// has and the attention kernels' second products wait for probabilities that never
-// come.  Only s4r_debug_waits changes them (so that tests can make a wait run
+// has, the attention kernels' second products wait for probabilities that never
+// come, and the projection's results wait for accumulators that never do.  Only s4r_debug_waits changes them (so that tests can make a wait run
 // out); they are read once per wait, on its slow path, or once per kernel.
 __device__ long long g_wait_limit = kWaitCycles;
 __device__ uint32_t g_barrier_unreachable = 0u;

@@ -6,8 +6,8 @@ import torch
 
 import rank_decode_attention_b200 as s4r
 from latent_reference import HALF_STEP, assert_within, cdiv, latent_attend, pack_page, quantise
-from test_gpu_latent import (check_latent, check_prefill, i32, latent_problem, prefill_problem, run_latent, run_prefill,
-                             status_words)
+from test_gpu_latent import (check_latent, check_prefill, check_project, i32, latent_problem, prefill_problem, run_latent,
+                             run_prefill, status_words)
 
 pytestmark = pytest.mark.gpu
 BF, DEV = torch.bfloat16, "cuda"
@@ -235,3 +235,22 @@ def test_prefill_waits_that_give_up(waits, dim, rope, vdim, limit, unreachable):
     s4r.s4r_prefill_attend(good["args"])
     assert s4r.s4r_read_device_status(None) == s4r.S4R_OK
     check_prefill(p, good, 0.1)
+
+
+@pytest.mark.parametrize("limit,unreachable", [(2_000_000, True), (1, True), (1, False), (2000, False)])
+@pytest.mark.parametrize("n,H,dim,rank,to_latent", [(1, 2, 64, 128, True), (3000, 24, 128, 512, False), (700, 100, 64, 256, True)])
+def test_project_waits_that_give_up(waits, n, H, dim, rank, to_latent, limit, unreachable):
+    g = torch.Generator().manual_seed(n)
+    n_in, n_out = (dim, rank) if to_latent else (rank, dim)
+    x = torch.randn(n, H, n_in, generator=g).to(BF)
+    basis = (torch.randn(H * dim, rank, generator=g) / math.sqrt(n_in)).to(BF)
+    xd, bd, out = x.to(DEV), basis.to(DEV), torch.empty(n, H, n_out, dtype=BF, device=DEV)
+    waits(limit, unreachable)
+    s4r.s4r_latent_project(xd, bd, out, to_latent=to_latent)
+    status = s4r.s4r_read_device_status(None)
+    waits(0, False)
+    assert status == s4r.S4R_ERR_TIMEOUT or (status == s4r.S4R_OK and not unreachable)
+    s4r.s4r_clear_device_status(None)
+    s4r.s4r_latent_project(xd, bd, out, to_latent=to_latent)
+    assert s4r.s4r_read_device_status(None) == s4r.S4R_OK
+    check_project(x, basis, out, H, dim, rank, to_latent)
