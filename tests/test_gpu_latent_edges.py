@@ -254,3 +254,82 @@ def test_project_waits_that_give_up(waits, n, H, dim, rank, to_latent, limit, un
     s4r.s4r_latent_project(xd, bd, out, to_latent=to_latent)
     assert s4r.s4r_read_device_status(None) == s4r.S4R_OK
     check_project(x, basis, out, H, dim, rank, to_latent)
+
+
+# ---------------------------------------------------------------- every kernel instance
+
+def project_width(n, H, dim, rank, to_latent, shared, sms=148):
+    """Columns a tile that the projection's rule chooses: rounds of the grid times (column groups a tile + 1)."""
+    out = rank if to_latent else dim
+    groups, cost = cdiv(out, 64), {}
+    for width in (256, 128, 64):
+        k = width // 64
+        tiles = cdiv(H * groups, k) if shared else H * cdiv(groups, k)
+        cost[width] = cdiv(tiles * cdiv(n, 128), sms) * (min(k, H * groups if shared else groups) + 1)
+    return min(cost, key=lambda w: (cost[w], -w))
+
+
+@pytest.mark.parametrize("n,H,dim,rank,to_latent,shared,width", [
+    (64, 128, 128, 512, True, False, 256), (64, 128, 128, 512, False, False, 256), (64, 128, 96, 512, True, False, 256),
+    (64, 128, 96, 512, False, False, 256), (3001, 32, 128, 512, False, True, 256), (3001, 32, 96, 512, False, True, 256),
+    (1500, 33, 256, 136, False, False, 256), (200, 100, 128, 448, True, True, 256), (1500, 33, 72, 136, False, True, 128),
+    (2500, 5, 96, 320, False, True, 128), (2000, 12, 128, 320, True, False, 128), (100, 74, 256, 512, False, False, 128)])
+def test_project_tiles_of_several_column_groups(n, H, dim, rank, to_latent, shared, width):
+    assert project_width(n, H, dim, rank, to_latent, shared) == width      # on a GPU of 148 multiprocessors
+    g = torch.Generator().manual_seed(n + dim)
+    n_in, n_out = (dim, rank) if to_latent else (rank, dim)
+    x = torch.randn(*((n, n_in) if shared else (n, H, n_in)), generator=g).to(BF)
+    basis = (torch.randn(H * dim, rank, generator=g) / math.sqrt(n_in)).to(BF)
+    wide = torch.full((n + 2, H, n_out + 16), 5.0, dtype=BF, device=DEV)
+    out = wide[1:n + 1, :, 8:8 + n_out]
+    s4r.s4r_latent_project(x.to(DEV), basis.to(DEV), out, to_latent=to_latent)
+    check_project(x, basis, out, H, dim, rank, to_latent)
+    assert (wide[0] == 5).all() and (wide[-1] == 5).all() and (wide[..., :8] == 5).all() and (wide[..., 8 + n_out:] == 5).all()
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("dim,vdim", [(64, 128), (40, 72), (8, 96)])
+def test_prefill_wide_values_beside_short_keys(dim, vdim, causal):
+    p = prefill_problem([1, 5, 0, 130, 257, 64], [1, 5, 3, 130, 1100, 65], 6, 2, dim, 0, vdim, seed=dim + vdim, pad=3)
+    d = run_prefill(p, 1.5 / math.sqrt(dim), causal)
+    check_prefill(p, d, 1.5 / math.sqrt(dim), causal)
+    assert (d["out"][-3:] == 77).all() and (d["lse"][-3:] == 77).all()
+    assert s4r.s4r_read_device_status(None) == s4r.S4R_OK
+
+
+# ---------------------------------------------------------------- 4-bit rows
+
+@pytest.mark.parametrize("change", ["page", "negative page", "length", "negative length"])
+def test_fp4_other_requests_beside_a_bad_one(change):
+    """The requests beside one with a bad length or page keep fp16's precision."""
+    p = latent_problem("fp4", [100, 50, 20, 64], 1, 4, 64, 16, seed=10)
+    q = dict(p, table=p["table"].clone(), lens=list(p["lens"]))
+    if change == "page":
+        q["table"][1, 2] = p["cache"].shape[0]
+    elif change == "negative page":
+        q["table"][1, 0] = -1
+    else:
+        q["lens"][1] = 16 * p["table"].shape[1] + 1 if change == "length" else -3
+    d = run_latent(q, 64, 0.2)
+    assert d["status"] == s4r.S4R_ERR_DEVICE
+    for b in (0, 2, 3):
+        out, lse, ob, lb = latent_attend(p["q"][b, 0].double(), p["rows"][b], p["lens"][b], 64, 0.2, HALF_STEP[torch.float16])
+        assert_within(d["out"][b, 0].cpu(), out, ob, f"request {b}")
+        assert_within(d["lse"][b, 0].cpu(), lse, lb, f"request {b}")
+
+
+@pytest.mark.parametrize("H", [5, 40])
+@pytest.mark.parametrize("n", [3, 64, 65, 20033])
+def test_fp4_rows_without_a_value_that_only_later_queries_see(n, H):
+    """The newest row has a group whose scale is NaN: queries that do not see it stay exact, the last one gets NaN."""
+    width, rank, page = 192, 160, 32
+    p = latent_problem("fp4", [n, 100], 3, H, width, page, seed=n)
+    at = n - 1
+    p["cache"][int(p["table"][0, at // page]), page * width // 2 + (at % page) * (width // 16) + 4] = 0x7f
+    d = run_latent(p, rank, 0.05)
+    assert d["status"] == s4r.S4R_OK
+    assert torch.isnan(d["out"][0, 2]).all() and torch.isnan(d["lse"][0, 2]).all()
+    for b, t, sees in ((0, 0, n - 2), (0, 1, n - 1), (1, 0, 98), (1, 1, 99), (1, 2, 100)):
+        out, lse, ob, lb = latent_attend(p["q"][b, t].double(), p["rows"][b], sees, rank, 0.05, HALF_STEP[torch.float16])
+        assert_within(d["out"][b, t].cpu(), out, ob, f"request {b} token {t}")
+        assert_within(d["lse"][b, t].cpu(), lse, lb, f"request {b} token {t}")
