@@ -333,3 +333,85 @@ def test_fp4_rows_without_a_value_that_only_later_queries_see(n, H):
         out, lse, ob, lb = latent_attend(p["q"][b, t].double(), p["rows"][b], sees, rank, 0.05, HALF_STEP[torch.float16])
         assert_within(d["out"][b, t].cpu(), out, ob, f"request {b} token {t}")
         assert_within(d["lse"][b, t].cpu(), lse, lb, f"request {b} token {t}")
+
+
+# ---------------------------------------------------------------- a captured step
+
+@pytest.mark.parametrize("dt", ["bf16", "fp4"])
+@pytest.mark.parametrize("B,T", [(5, 1), (1100, 1), (40, 3)])
+def test_captured_decode_steps(B, T, dt):
+    """Plan, write, absorb, attend and expand captured as one graph and replayed step by step: each step equals the same
+    calls made one by one, and the last one 64-bit attention over the rows written."""
+    H, dim, rope, rank, page, steps = 6, 64, 32, 160, 16, 4
+    width, n = rank + rope, B * T
+    g = torch.Generator().manual_seed(B + T)
+    bk = (torch.randn(H * dim, rank, generator=g) / 8).to(BF).to(DEV)
+    old = torch.randint(0, 90, (B,), generator=g).int()
+    cols = cdiv(90 + steps * T, page)
+    pages = B * cols
+    pool = torch.randperm(pages, generator=g).int()
+    new_rows = torch.randn(steps, n, width, generator=g).to(BF)
+    new_q = torch.randn(steps, n, H, dim + rope, generator=g).to(BF)
+    first = torch.randn(pages * page, width, generator=g).to(BF)
+
+    def state():
+        table = torch.full((B, cols), -1, dtype=torch.int32)
+        have = [cdiv(int(x), page) for x in old]
+        at = pages
+        for b in range(B):
+            table[b, :have[b]] = pool[at - have[b]:at]
+            at -= have[b]
+        cache = (torch.zeros(pages, page, width, dtype=BF, device=DEV) if dt == "bf16"
+                 else torch.zeros(pages, page * width * 9 // 16, dtype=torch.uint8, device=DEV))
+        s4r.s4r_latent_write(latents=first.to(DEV), slots=torch.arange(pages * page, device=DEV), cache=cache, page_size=page)
+        s = dict(table=table.to(DEV), cache=cache, pool=pool.to(DEV), free=i32([at]), held=old.to(DEV), new=i32([T] * B),
+                 cu=i32([0] * (B + 1)), slots=torch.zeros(n, dtype=torch.int64, device=DEV), rows=new_rows[0].to(DEV),
+                 q=new_q[0].to(DEV), ql=torch.zeros(B, T, H, width, dtype=BF, device=DEV), w=status_words(),
+                 ol=torch.zeros(B, T, H, rank, dtype=BF, device=DEV), out=torch.zeros(n, H, dim, dtype=BF, device=DEV))
+        args = dict(q=s["ql"], cache=cache, block_table=s["table"], lengths=s["held"], out=s["ol"], page_size=page, scale=0.1)
+        s["ws"] = torch.empty(s4r.s4r_latent_attend_workspace_bytes(s4r.latent_attend_args(**args)), dtype=torch.uint8, device=DEV)
+        s4r.s4r_workspace_init(s["ws"])
+        s["args"] = s4r.latent_attend_args(**args, workspace=s["ws"])
+        return s
+
+    def step(s, wait=lambda: None):
+        s4r.s4r_page_plan(lengths=s["held"], new_tokens=s["new"], block_table=s["table"], free_pages=s["pool"],
+                          free_count=s["free"], lengths_out=s["held"], free_count_out=s["free"], cu_tokens=s["cu"],
+                          slots=s["slots"], page_size=page, status_workspace=s["w"])
+        wait()
+        s4r.s4r_latent_write(latents=s["rows"], slots=s["slots"], cache=s["cache"], page_size=page, status_workspace=s["w"])
+        wait()
+        ql = s["ql"].view(n, H, width)
+        ql[..., rank:] = s["q"][..., dim:]
+        s4r.s4r_latent_project(s["q"][..., :dim], bk, ql[..., :rank], to_latent=True)
+        wait()
+        s4r.s4r_latent_attend(s["args"])
+        wait()
+        s4r.s4r_latent_project(s["ol"].view(n, H, rank), bk, s["out"], to_latent=False)
+        wait()
+
+    a, b = state(), state()
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        step(a)
+    for k in range(steps):
+        for s in (a, b):
+            s["rows"].copy_(new_rows[k])
+            s["q"].copy_(new_q[k])
+        graph.replay()
+        step(b, torch.cuda.synchronize)
+        torch.cuda.synchronize()
+        for key in ("table", "free", "held", "cu", "slots", "cache", "ql", "ol", "out"):
+            assert torch.equal(a[key], b[key]), (k, key)
+    for s in (a, b):
+        assert s4r.s4r_read_device_status(s["w"]) == s4r.S4R_OK and s4r.s4r_read_device_status(s["ws"]) == s4r.S4R_OK
+    exact = (first if dt == "bf16" else quantise(first)[2]).double()
+    fresh = [(new_rows[k] if dt == "bf16" else quantise(new_rows[k])[2]).double() for k in range(steps)]
+    table, half = a["table"].cpu().long(), HALF_STEP[BF if dt == "bf16" else torch.float16]
+    for r in range(0, B, max(1, B // 20)):
+        pos = torch.arange(int(old[r]))
+        rows = torch.cat([exact[table[r, pos // page] * page + pos % page]] + [f[r * T:(r + 1) * T] for f in fresh]).to(DEV)
+        for t in range(T):
+            out, _, ob, _ = latent_attend(a["ql"][r, t].double(), rows, len(rows) - T + 1 + t, rank, 0.1, half)
+            assert_within(a["ol"][r, t], out, ob, f"request {r} token {t}")
