@@ -176,7 +176,8 @@ s4r_status prefill_launch(const CUtensorMap &mq, const CUtensorMap &mqr, const C
   const size_t smem = pf_smem_bytes(KC);
   const cudaError_t err = ensure_smem<prefill_attend_kernel<KC, VC>>(smem);
   if (err != cudaSuccess) return fail("prefill_attend_kernel (shared memory)", err);
-  const dim3 grid((unsigned)p.hq, (unsigned)p.batch, (unsigned)ceil_div(p.max_q, 2 * kPfTile));
+  // at least one block a sequence, which reports what max_q leaves out
+  const dim3 grid((unsigned)p.hq, (unsigned)p.batch, grid_of(ceil_div(p.max_q, 2 * kPfTile), 65535));
   prefill_attend_kernel<KC, VC><<<grid, kPfThreads, smem, st>>>(mq, mqr, mk, mkr, mv, p);
   return check_launch("prefill_attend_kernel");
 }
@@ -376,7 +377,7 @@ s4r_status s4r_prefill_attend(const s4r_prefill_attend_args *a, void *stream) {
       a->rope_dim > 64 || a->batch > 65535 || a->n_heads_q > 65535 || a->max_q > 65535 * 2 * kPfTile || a->total_q > INT32_MAX - 2 * kPfTile ||
       a->total_k > INT32_MAX - 2 * kPfTile)
     return S4R_ERR_UNSUPPORTED;
-  if (a->batch == 0 || a->total_q == 0 || a->max_q == 0) return S4R_OK;
+  if (a->batch == 0 || a->total_q == 0) return S4R_OK;
   const void *must[] = {a->q, a->cu_q, a->cu_k, a->out};
   for (const void *p : must)
     if (!p || !aligned16(p)) return S4R_ERR_INVALID_ARG;

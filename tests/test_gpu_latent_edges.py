@@ -415,3 +415,15 @@ def test_captured_decode_steps(B, T, dt):
         for t in range(T):
             out, _, ob, _ = latent_attend(a["ql"][r, t].double(), rows, len(rows) - T + 1 + t, rank, 0.1, half)
             assert_within(a["ol"][r, t], out, ob, f"request {r} token {t}")
+
+
+def test_prefill_reports_rows_that_a_limit_of_zero_leaves_out():
+    p = prefill_problem([3, 0], [3, 4], 2, 1, 64, 0, 64, seed=1)
+    d = run_prefill(p, 0.1, max_q=0)
+    assert s4r.s4r_read_device_status(None) == s4r.S4R_ERR_DEVICE
+    s4r.s4r_clear_device_status(None)
+    assert (d["out"] == 77).all() and (d["lse"] == 77).all()
+    p = prefill_problem([0, 0], [5, 0], 2, 1, 64, 0, 64, seed=1, pad=4)         # rows, but none of a sequence
+    d = run_prefill(p, 0.1, max_q=0)
+    assert s4r.s4r_read_device_status(None) == s4r.S4R_OK
+    assert (d["out"] == 77).all() and (d["lse"] == 77).all()
