@@ -26,10 +26,11 @@
 //   warp 0     one thread copies tiles with TMA: 128 columns x 64 tokens a
 //              ring slot, one box a page and 64 columns; and the unit's
 //              queries;
-//   warp 1     one thread issues tcgen05.mma: S^T of tile i + 1, as far as the
-//              ring holds it, before O^T of tile i, so the softmax of one tile
-//              runs beside the products of another; slots are released column
-//              block by column block;
+//   warp 1     one thread issues tcgen05.mma: O^T of tile i as soon as its
+//              probabilities are there, until then S^T of tile i + 1 as far as
+//              the ring holds it, so the softmax of one tile runs beside the
+//              products of another; slots are released column block by column
+//              block;
 //   warps 2-9  softmax: probabilities against a reference maximum that moves
 //              only when a logit exceeds it by more than 2^8 (then O^T is
 //              rescaled in TMEM), sums in fp32, P^T into shared memory; at the
@@ -42,12 +43,15 @@
 // the second product; the sum that divides it is not.
 //
 // Measured (width 576, rank 512): a CTA takes a tile in 1.64 us with 16 heads
-// (together 6.65 TB/s, the rate of a copy), 1.9 us with 64, 2.0 us from 4-bit
-// rows, where shared memory is the limit: fp16 rows are written once and read by
-// two products.  32 ragged requests of 8250 rows on average, 64 heads: 85 us;
-// 8 requests of 32K, 128 heads, two query tokens: 236 us; 4-bit, 5 requests up
-// to 128K, 20 heads: 95 us; one request of 8K, 16 heads: 15.4 us, of which 12
-// are one tile's chain of latencies and the rest the join of 128 parts.
+// (together 6.65 TB/s, the rate of a copy) and 1.9 us with 64; from 4-bit rows in
+// 2.0, 2.1 and 2.4 us with 16, 32 and 64.  What paces those is not known: the
+// products' own rates make it 0.8 us and the passage through shared memory 0.5,
+// slots handed on without conversion took 2.1 us, a ring of 6 slots instead of 9
+// 2% more (both 16 heads).  Whole calls through the binding, inputs changing: 32
+// ragged requests of 8250 rows on average, 64 heads 88 us; 8 requests of 32K, 128
+// heads, two query tokens 230 us; 4-bit, 5 requests up to 128K, 20 heads 96 us;
+// one request of 8K, 16 heads 15.5 us, of which 12 are one tile's chain of
+// latencies and the rest the join of 128 parts.
 //
 // Every wait is bounded (umma.cuh); a wait that gives up sets the status word
 // and ends its role, and every other role then runs out too.  The producer and

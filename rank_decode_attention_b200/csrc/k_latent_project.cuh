@@ -18,9 +18,11 @@
 // issued has ended.  The weights are K-major when latents are
 // expanded and N-major when queries are absorbed; the descriptors say which.
 //
-// Measured: 64 tokens, 128 heads, 128 -> 512: 6.6 us (4.1 TB/s); 8190 tokens with
-// one latent for 32 heads, 512 -> 128: 30.0 us, 1.14 PFLOP/s, bound by the 384 KB
-// of operands that a 128 x 256 tile takes from L2 (13 TB/s together).
+// Measured: 64 tokens, 128 heads, 128 -> 512: 6.9 us on the device (3.9 TB/s);
+// 8190 tokens with one latent for 32 heads, 512 -> 128: 39 us through the binding
+// with inputs changing, 0.88 PFLOP/s (32.4 us in a graph over three input sets,
+// 1.06), bound by the 384 KB of operands that a 128 x 256 tile takes from L2 (10
+// to 12 TB/s together).
 #pragma once
 #include "umma.cuh"
 

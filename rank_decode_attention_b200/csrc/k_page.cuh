@@ -18,10 +18,10 @@ namespace s4r {
 // a few microseconds out of L2), keeps them in shared memory and then serves
 // its share of the tokens and of the new pages, each found by binary search.
 // So no CTA waits for another one, and one request with all the tokens is
-// spread as well as many with one.  Latency is all there is to it: 5.9 us for
-// 256 requests with a token each (one CTA), 10.7 us for 1001 requests with 619
-// thousand tokens (147 CTAs and the commit kernel; the 10 MB written would take
-// 1.5 us).
+// spread as well as many with one.  Latency is most of it: 5.6 us on the device
+// for 256 requests with a token each (one CTA), 10.8 us for 1001 requests with 600
+// thousand tokens (a CTA on each of 148 multiprocessors and the commit kernel;
+// the 10 MB written would take 1.5 us).
 struct PagePlan {
   int32_t batch, page_size, page_shift, max_pages, free_capacity;
   int64_t max_tokens;
@@ -274,9 +274,9 @@ __global__ void __launch_bounds__(kWriteThreads) latent_write_bf16(const LatentW
 // and the scale 4, so x / scale is either exactly a border between two codes
 // (at most 3 bits) or a part in 2^15 away from every border; the product with
 // the rounded reciprocal is within 2^-22 of it, and rounded to 20 bits it is on
-// the border, or on the same side of it, as the quotient is.  (With divisions
-// the 32765 rows of 576 columns took 21.4 us, 16 x 9 instructions a group; now
-// 17.7 us, 4.9 TB/s.)
+// the border, or on the same side of it, as the quotient is.  (32765 rows of 576
+// columns, the same ones each time: 21.4 us with divisions, 16 x 9 instructions a
+// group, now 17.7 us; with inputs changing 22.5 us, 3.8 TB/s.)
 template <bool ONE>
 __global__ void __launch_bounds__(kWriteThreads) latent_write_fp4(const LatentWrite p) {
   const uint32_t per = (uint32_t)p.width / 16;

@@ -26,9 +26,10 @@
 // that gave up every role runs out, the producer and the issuer when what they
 // issued has ended.
 //
-// Measured: one prompt of 8192, 16 heads, 128 + 64 | 128: 301 us, 1.14 PFLOP/s;
-// six prompts of 33 to 2900 behind a prefix of 517, 32 over 8 heads, 128 | 128:
-// 388 us, 0.61 PFLOP/s.  A step of 256 queries x 128 keys takes some 4400 cycles,
+// Measured through the binding, inputs changing: one prompt of 8192, 16 heads,
+// 128 + 64 | 128: 360 us, 0.95 PFLOP/s (303 us before the power cap settles); six
+// prompts of 33 to 2900 behind a prefix of 517, 32 over 8 heads, 128 | 128: 400
+// us, 0.59 PFLOP/s (385 before).  A step of 256 queries x 128 keys takes some 4400 cycles,
 // of which the products need 2600, the exponentials of both tiles 2048 of the
 // special-function unit, and about 900 are waits for K and V (a ring of 8 chunks
 // beside 96 KB of queries).  Exponentials by polynomial on the multiply-add
