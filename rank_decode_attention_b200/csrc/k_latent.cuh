@@ -1086,7 +1086,7 @@ __global__ void __launch_bounds__(kLcThreads) latent_combine_kernel(const Latent
       const float2 ml = p.ml[slot_of(base + threadIdx.x)];
       // a part that saw nothing has no reference
       f = ml.x == -CUDART_INF_F && ml.y == 0.0f ? 0.0f : exp2f(ml.x - top);
-      part_sum = f == 0.0f ? 0.0f : f * ml.y;
+      part_sum = f * ml.y;   // also of weight 0: a NaN in a part's sum is one in the row's
     }
     part_sum = warp_sum(part_sum);
     __syncthreads();

@@ -427,3 +427,41 @@ def test_prefill_reports_rows_that_a_limit_of_zero_leaves_out():
     d = run_prefill(p, 0.1, max_q=0)
     assert s4r.s4r_read_device_status(None) == s4r.S4R_OK
     assert (d["out"] == 77).all() and (d["lse"] == 77).all()
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp4"])
+@pytest.mark.parametrize("case", ["a part of nothing else", "a part that weighs nothing"])
+def test_latent_nan_logits_reach_the_joined_result(case, dt):
+    """Logits of NaN make a query's result NaN, wherever the request is cut: also where one CTA saw nothing else, and
+    where all else that it saw weighs nothing beside another part's."""
+    n, H, width, page = 30000, 5, 64, 64
+    p = latent_problem(dt, [n, 100], 1, H, width, page, seed=7)
+    if case == "a part that weighs nothing":            # 256 above the others
+        p["q"][0, 0, :, 16:32], p["q"][0, 0, :, 40] = 0.0, 0.0
+        p["q"][0, 0, :, 16] = 8.0
+        top, bad = torch.zeros(1, width), [20000]
+        top[0, 16] = 6.0 * 16
+        codes, scales, _ = quantise(top.to(BF))
+        at = 100
+        if dt == "bf16":
+            p["cache"][int(p["table"][0, at // page]), at % page] = top[0].to(BF)
+        else:
+            pg = p["cache"][int(p["table"][0, at // page])]
+            pg[at % page * (width // 2):(at % page + 1) * (width // 2)] = codes[0, 0::2] | (codes[0, 1::2] << 4)
+            first = page * width // 2 + at % page * (width // 16)
+            pg[first:first + width // 16] = scales[0]
+    else:
+        bad = range(12032, 12288)         # on 148 multiprocessors: the four tiles of one CTA
+    for at in bad:
+        pg = p["cache"][int(p["table"][0, at // page])]
+        if dt == "bf16":
+            pg[at % page, 35] = math.nan
+        else:
+            pg[page * width // 2 + at % page * (width // 16) + 2] = 0x7f
+    d = run_latent(p, width, 0.35)
+    assert d["status"] == s4r.S4R_OK
+    assert torch.isnan(d["out"][0]).all() and torch.isnan(d["lse"][0]).all()
+    step = HALF_STEP[BF if dt == "bf16" else torch.float16]
+    out, lse, ob, lb = latent_attend(p["q"][1, 0].double(), p["rows"][1], 100, width, 0.35, step)
+    assert_within(d["out"][1, 0].cpu(), out, ob)
+    assert_within(d["lse"][1, 0].cpu(), lse, lb)
