@@ -1084,9 +1084,11 @@ __global__ void __launch_bounds__(kLcThreads) latent_combine_kernel(const Latent
     float f = 0.0f, part_sum = 0.0f;
     if ((int)threadIdx.x < m) {
       const float2 ml = p.ml[slot_of(base + threadIdx.x)];
-      // a part that saw nothing has no reference
-      f = ml.x == -CUDART_INF_F && ml.y == 0.0f ? 0.0f : exp2f(ml.x - top);
-      part_sum = f * ml.y;   // also of weight 0: a NaN in a part's sum is one in the row's
+      // No part weighs less than the least positive value: what is not finite in
+      // its sums is not in the row either.  (That also is the weight where no
+      // part has a reference, exp2 of NaN.)
+      f = fmaxf(exp2f(ml.x - top), __uint_as_float(1u));
+      part_sum = f * ml.y;
     }
     part_sum = warp_sum(part_sum);
     __syncthreads();
@@ -1110,7 +1112,7 @@ __global__ void __launch_bounds__(kLcThreads) latent_combine_kernel(const Latent
 #pragma unroll
       for (int n = 0; n < N; ++n) {
         const float w = i0 + n * W < m ? f_s[i0 + n * W] : 0.0f;
-        if (w != 0.0f) {   // a part of weight 0 may hold infinities
+        if (w != 0.0f) {
 #pragma unroll
           for (int k = 0; k < K; ++k) {
             o[k].x = fmaf(w, x[n][k].x, o[k].x);

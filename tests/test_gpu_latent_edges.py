@@ -465,3 +465,27 @@ def test_latent_nan_logits_reach_the_joined_result(case, dt):
     out, lse, ob, lb = latent_attend(p["q"][1, 0].double(), p["rows"][1], 100, width, 0.35, step)
     assert_within(d["out"][1, 0].cpu(), out, ob)
     assert_within(d["lse"][1, 0].cpu(), lse, lb)
+
+
+@pytest.mark.parametrize("n,at", [(30000, 20000), (30000, 29990), (200, 150)])
+def test_latent_infinite_values_of_weight_zero(n, at):
+    """A row whose infinity makes its logit minus infinity has weight 0: its column is 0 times infinity, the others are
+    exact, also where the rest of its part weighs nothing beside another part's."""
+    H, width, page = 5, 64, 64
+    p = latent_problem("bf16", [n, 100], 1, H, width, page, seed=8)
+    p["q"][0, 0, :, 16], p["q"][0, 0, :, 35] = 8.0, -0.5
+    flat = p["cache"].view(-1, width)
+    row = lambda i: int(p["table"][0, i // page]) * page + i % page  # noqa: E731
+    flat[row(100)] = 0.0
+    flat[row(100), 16] = 96.0
+    flat[row(at), 35] = math.inf
+    rows = p["rows"][0].clone()
+    rows[100] = flat[row(100)].double()
+    live = torch.cat([rows[:at], rows[at + 1:]])
+    d = run_latent(p, width, 0.35)
+    assert d["status"] == s4r.S4R_OK
+    assert torch.isnan(d["out"][0, 0, :, 35]).all()
+    out, lse, ob, lb = latent_attend(p["q"][0, 0].double(), live, n - 1, width, 0.35, HALF_STEP[BF])
+    keep = [c for c in range(width) if c != 35]
+    assert_within(d["out"][0, 0][:, keep].cpu(), out[:, keep], ob[:, keep])
+    assert_within(d["lse"][0, 0].cpu(), lse, lb)
