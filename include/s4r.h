@@ -477,7 +477,8 @@ s4r_status s4r_latent_project(const s4r_latent_project_args *args, void *stream)
  * max_q must be at least the longest query count; it only sizes the launch.
  * Device status (the library-wide word, s4r_read_device_status(NULL, .)):
  * offsets that decrease or leave [0, total] (the sequence is skipped), a
- * sequence longer than max_q (its rows from max_q on are not computed). */
+ * sequence longer than max_q (its rows from max_q on are not computed);
+ * S4R_ERR_TIMEOUT as elsewhere. */
 typedef struct {
   int32_t batch;                         /* <= 65535 */
   int32_t n_heads_q, n_heads_kv;

@@ -514,8 +514,9 @@ def s4r_read_device_status(workspace, stream=None) -> int:
 
 def s4r_debug_waits(limit_cycles: int = 0, unreachable_barrier: bool = False) -> int:
     """Testing hook: limit of the device-side bounded waits (SM cycles, 0 =
-    default) and the switch that makes the scoring kernel's grid barrier
-    unreachable (see include/s4r.h)."""
+    default) and the switch that makes the scoring kernel's grid barrier and a
+    signal in each kernel of latent attention, prefill attention and the
+    projection unreachable (see include/s4r.h)."""
     return _check(lib().s4r_debug_waits(int(limit_cycles), 1 if unreachable_barrier else 0),
                   "s4r_debug_waits")
 
